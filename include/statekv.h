@@ -306,6 +306,85 @@ int statekv_step_noalloc(int Hq, int Hkv, int d, int T, int B, int dtype, int ma
                          int32_t* posc_new, float* scorec_new, void* kd, void* vd,
                          int32_t* posd, int d_len, int max_tok, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A key/value cache held in 4 bits (caller-owned device memory).
+ *
+ * Per token, KV head and group of 64 consecutive channels, keys and values
+ * alike, a value x is held as a code c in 0..15 that stands for m + c * s:
+ *   m = the group's smallest value rounded down to bfloat16,
+ *   s = (largest - m) / 15 rounded up to bfloat16,
+ *   c = the integer nearest to (x - m) / s, ties to even (0 where s = 0),
+ * so the error is at most s / 2 and a group of equal bfloat16 values is exact.
+ * With s and m that is 4.5 bits a value.  A group that holds a NaN or an
+ * infinity reads back as NaN.
+ *
+ * The cache is one buffer of statekv_q4_bytes bytes (16-byte aligned) for
+ * n_streams sequences of up to `capacity` tokens each; its inner layout is the
+ * library's.  It needs no initial value: what no append has written is never
+ * read as long as lengths and ranges stay within what was written.  Token
+ * numbers are cache tokens 0 .. capacity-1 in every call.
+ *
+ * Conventions as above.  Calls that write the same cache, or write it while
+ * another reads it, must be ordered by the caller (tokens share words).  No
+ * call allocates memory, keeps state or reads a device value on the host, so
+ * all can be captured into a CUDA graph.  Outputs must not overlap inputs. */
+
+/* Bytes of a cache; negative statekv_status on a bad shape (INVALID_ARG,
+ * UNSUPPORTED: d not in {64,128}, capacity above 2^30). */
+long long statekv_q4_bytes(int n_streams, int Hkv, int d, int capacity);
+
+/* Quantise k, v [S][n][Hkv][d] (dtype) into cache tokens start .. start+n-1 of
+ * every stream; other tokens keep their values.  With starts (device int32
+ * [S], or NULL) stream s begins at starts[s] instead, and tokens that fall
+ * outside [0, capacity) are dropped.  n = 0 does nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (start + n > capacity), CUDA. */
+int statekv_q4_append(void* cache, int n_streams, int Hkv, int d, int capacity, const void* k,
+                      const void* v, int n, int dtype, int start, const int32_t* starts,
+                      void* stream);
+
+/* Read cache tokens start .. start+n-1 of every stream back into k, v
+ * [S][n][Hkv][d] (dtype): m + c * s in float32, rounded once for bf16.  With
+ * starts (device int32 [S], or NULL) stream s begins at starts[s] instead, and
+ * the rows of tokens outside [0, capacity) are left as they were.
+ * Errors: as statekv_q4_append. */
+int statekv_q4_read(const void* cache, int n_streams, int Hkv, int d, int capacity, int start,
+                    const int32_t* starts, int n, int dtype, void* k, void* v, void* stream);
+
+/* Attention of n_text tokens over a 4-bit cache and causally over themselves
+ * (statekv_decode over such a cache, with an optional window):
+ *   q [S][n_text][Hq][d], k,v [S][n_text][Hkv][d], out [S][n_text][Hq][d]
+ *   (dtype); lse [S][Hq][n_text] float32 natural-log, or NULL.
+ * Stream s holds L tokens: `length`, or lengths[s] (device int32 [S], or NULL;
+ * clipped to [0, capacity]).  Text token i stands at position L + i and sees
+ * cache tokens 0 .. L-1 and text tokens 0 .. i; with window > 0 only positions
+ * above L + i - window and those below n_sink (window = 0: no window, n_sink
+ * unused).  Scale 1/sqrt(d).  A key or value the mask hides has no influence,
+ * whatever it holds.  The text tokens are not written to the cache.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int statekv_q4_decode(const void* cache, int n_streams, int Hq, int Hkv, int d, int capacity,
+                      const void* q, const void* k, const void* v, int n_text, int dtype,
+                      int length, const int32_t* lengths, int window, int n_sink, void* out,
+                      float* lse, void* stream);
+
+/* Causal self-attention over n_tokens tokens with a sliding window and first
+ * tokens that stay visible: token i attends to the tokens j <= i with
+ * j > i - window or j < n_sink.  (The windowed counterpart of
+ * full_causal_prefill, which it equals for window >= n_tokens.)
+ *   q [n_tokens][Hq][d], k,v [n_tokens][Hkv][d], out [n_tokens][Hq][d] (device,
+ *   dtype); lse [Hq][n_tokens] float32 natural-log (device) or NULL.
+ * window >= 1, n_sink >= 0.  Work grows with n_tokens x (window + n_sink).  A
+ * key or value the mask hides has no influence, whatever it holds.  No memory
+ * is allocated.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int sink_window_prefill(const void* q, const void* k, const void* v, int n_tokens, int Hq, int Hkv,
+                        int d, int dtype, int window, int n_sink, void* out, float* lse,
+                        void* stream);
+
+/* sink_window_prefill over n_seq independent sequences of n_tokens each: every
+ * tensor gains a leading [n_seq] dimension (lse: [n_seq][Hq][n_tokens]). */
+int sink_window_prefill_batched(const void* q, const void* k, const void* v, int n_seq,
+                                int n_tokens, int Hq, int Hkv, int d, int dtype, int window,
+                                int n_sink, void* out, float* lse, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -129,4 +129,38 @@ struct GatherArgs {
   int S;
 };
 
+// Append to, or read from, the 4-bit cache (q4_cache.cuh).
+struct Q4IoArgs {
+  void* cache;               // [S][Hkv][cap_blk] blocks
+  const void* k;             // append: [S][n][Hkv][d]
+  const void* v;
+  void* k_out;               // read: [S][n][Hkv][d]
+  void* v_out;
+  const int32_t* starts;     // [S] first cache token per stream (device), or null: `start`
+  int start, n, S, Hkv, capacity;
+  int cap_blk, n_blk;        // 32-token blocks per (stream, KV head); thread blocks per (stream, KV head)
+};
+
+// Causal attention of n tokens with a sliding window (0: none) and first
+// tokens that stay visible, over an optional 4-bit cache and the n tokens
+// themselves.
+struct WindowArgs {
+  const void* q;             // [S][n][Hq][d]
+  const void* k;             // [S][n][Hkv][d]
+  const void* v;
+  void* out;                 // [S][n][Hq][d]
+  float* lse;                // [S][Hq][n] natural log, may be null
+  const void* cache;         // null: the sequence alone
+  const int32_t* lengths;    // [S] cached tokens per stream (device), or null: `length`
+  int length, capacity, cap_blk;
+  int n, S, Hq, Hkv, window, n_sink;
+  float scale_log2;          // log2(e)/sqrt(d)
+};
+
+// Cached tokens of stream s, clipped to the cache.
+__device__ __forceinline__ int q4_length(const WindowArgs& a, int s) {
+  const int L = a.lengths ? __ldg(a.lengths + s) : a.length;
+  return min(max(L, 0), a.capacity);
+}
+
 }  // namespace skv

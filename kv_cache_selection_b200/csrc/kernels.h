@@ -110,6 +110,12 @@ cudaError_t launch_attn_combine(const AttnTcArgs& a, int d, cudaStream_t st, boo
 cudaError_t launch_attn_merge_wide(const AttnTcArgs& a, int d, int n_sm, cudaStream_t st, bool pdl = false);
 MergeArgs merge_args(const AttnTcArgs& a, int d);
 
+// 4-bit cache: append and read back; attention over it (and, with no cache, over
+// a sequence alone) on the CUDA cores.
+cudaError_t launch_q4_append(Q4IoArgs a, int dtype, int d, cudaStream_t st, bool pdl = false);
+cudaError_t launch_q4_read(Q4IoArgs a, int dtype, int d, cudaStream_t st);
+cudaError_t launch_window_simt(const WindowArgs& a, int dtype, int d, cudaStream_t st);
+
 // Message for statekv_last_error(NULL) (errors of calls without a handle).
 void set_free_error(const char* msg);
 

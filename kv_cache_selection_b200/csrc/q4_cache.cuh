@@ -1,0 +1,86 @@
+// Layout and arithmetic of the 4-bit key/value cache.
+//
+// Quantisation, per token, KV head and group of 64 consecutive channels (keys
+// and values alike):
+//   m = the group's smallest value, rounded down to bfloat16,
+//   s = (largest - m) / 15, rounded up to bfloat16,
+//   c = the integer nearest to (x - m) / s, ties to even (0 where s = 0),
+// so c is in 0..15 and x ~ m + c s with an error of at most s / 2.  Rounding m
+// down and s up keeps the whole group inside [m, m + 15 s]; bfloat16 keeps the
+// range of the inputs, at 4 + 32 / 64 = 4.5 bits a value.  c * s is exact in
+// float32 (4 x 8 bits), so m + c s is one rounding.  A group that holds a NaN
+// or an infinity (or whose m leaves bfloat16's range) stores s = m = NaN and
+// reads back as NaN.
+//
+// The cache is [S][Hkv][ceil(capacity / 32)] blocks of 32 tokens, a block one
+// contiguous run of bytes:
+//   K codes  [32 tokens][D/2 bytes]      16 D bytes
+//   V codes  [D/32 chunks][32 lanes][16]  16 D bytes
+//   K scales [32 tokens][D/64]            4 bytes each: s in the low half, m in the high
+//   V scales [32 tokens][D/64]
+// The code words are laid out as the fragments of an m16n8k16 tensor-core
+// product with 16 tokens (K) or 16 channels (V) as its rows, lane = 4 gid + tig:
+//   K: token row, tig's 4 (D=128) or 2 (D=64) words; word w holds channels
+//      64 (w/2) + 16 tig + 8 (w%2) + 0..7;
+//   V: word (channel d, tig) holds the tokens {2 tig, 2 tig + 1, 8 + 2 tig,
+//      9 + 2 tig} and the same + 16; d = 8 j + gid sits in chunk j/4, lane
+//      4 gid + tig, word j%4.
+// Inside a word the eight codes are four pairs (field f: codes 2f in the low
+// half, 2f + 1 in the high half) placed so that one shift or rotation and one
+// and-or turn a pair into two fp16 numbers 16 + c (code at mantissa bits 6..9).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace skv {
+
+constexpr int kQ4Tokens = 32;  // tokens per block
+constexpr int kQ4Group = 64;   // channels per scale
+
+template <int D>
+struct Q4Block {
+  static constexpr int kGroups = D / kQ4Group;
+  static constexpr int kRow = D / 2;                      // K code bytes of a token
+  static constexpr int kV = kQ4Tokens * kRow;             // V codes
+  static constexpr int kKs = 2 * kV;                      // K scales
+  static constexpr int kVs = kKs + kQ4Tokens * kGroups * 4;
+  static constexpr int kBytes = kVs + kQ4Tokens * kGroups * 4;  // 4608 (D=128), 2304 (D=64)
+};
+
+__host__ __device__ constexpr int q4_block_bytes(int d) { return 32 * d + 256 * (d / kQ4Group); }
+
+constexpr uint32_t kQ4Mask = 0x03C003C0u;
+
+// pairs (code 2f | code 2f+1 << 16), f = 0..3 -> word
+__host__ __device__ __forceinline__ uint32_t q4_pack(uint32_t p0, uint32_t p1, uint32_t p2, uint32_t p3) {
+  const uint32_t r = p3 << 6;
+  return (p0 << 6) | (p1 << 10) | (p2 << 2) | ((r >> 8) | (r << 24));
+}
+// field f of a word, each code at bits 6..9 of its half
+template <int F>
+__device__ __forceinline__ uint32_t q4_field(uint32_t x) {
+  if (F == 1) x >>= 4;
+  if (F == 2) x <<= 4;
+  if (F == 3) x = __funnelshift_l(x, x, 8);
+  return x & kQ4Mask;
+}
+// code i (0..7) of a word
+__device__ __forceinline__ int q4_code(uint32_t x, int i) {
+  const int f = i >> 1;
+  x = f == 0 ? x : f == 1 ? x >> 4 : f == 2 ? x << 4 : __funnelshift_l(x, x, 8);
+  return (int)((x >> (6 + 16 * (i & 1))) & 15u);
+}
+
+__device__ __forceinline__ float q4_scale(uint32_t sm) { return __uint_as_float(sm << 16); }
+__device__ __forceinline__ float q4_min(uint32_t sm) { return __uint_as_float(sm & 0xffff0000u); }
+
+// Byte offset of the V word of (channel d, tig) within a block.
+__device__ __forceinline__ int q4_v_word(int d, int tig) {
+  const int j = d >> 3;
+  return (j >> 2) * 512 + ((d & 7) * 4 + tig) * 16 + (j & 3) * 4;
+}
+
+}  // namespace skv

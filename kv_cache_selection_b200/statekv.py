@@ -58,6 +58,12 @@ _SIGS = {
     "statekv_decode": (_i, [_vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp]),
     "full_causal_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
     "full_causal_prefill_batched": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "statekv_q4_bytes": (ctypes.c_longlong, [_i, _i, _i, _i]),
+    "statekv_q4_append": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp]),
+    "statekv_q4_read": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
+    "statekv_q4_decode": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
+    "sink_window_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "sink_window_prefill_batched": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -309,4 +315,172 @@ def full_causal_prefill(q, k, v, out=None, lse=None, with_lse=True, stream=None)
                                          code, out.data_ptr(), lse.data_ptr() if lse is not None else None,
                                          _stream_ptr(stream))
     _check(rc)
+    return out, lse
+
+
+class _device:
+    """Makes a tensor's device the current one for a call (nothing to do where
+    it already is)."""
+
+    __slots__ = ("dev", "back")
+
+    def __init__(self, dev):
+        self.dev, self.back = dev, -1
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.dev:
+            torch.cuda.set_device(self.dev)
+            self.back = now
+
+    def __exit__(self, *exc):
+        if self.back >= 0:
+            torch.cuda.set_device(self.back)
+
+
+def _empty(shape, dtype, dev, stream):
+    """A new tensor for work on `stream` (allocated for that stream, so that
+    its memory is not still in use by work queued elsewhere)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_ptr(stream), device=dev)
+    with torch.cuda.stream(st):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+class Q4Cache:
+    """Keys and values of n_streams sequences in 4.5 bits a value (one layer).
+
+    A group of 64 channels of a token's key or value keeps codes 0..15, a scale
+    and a smallest value (include/statekv.h has the rounding).  The buffer is a
+    torch tensor, `data`, that this object owns; every call runs on `stream`, or
+    on the current stream.  Leading [S] dimensions of q, k and v may be left out
+    when n_streams is 1.
+    """
+
+    def __init__(self, Hkv, d, capacity, n_streams=1, device=None):
+        n = lib.statekv_q4_bytes(n_streams, Hkv, d, capacity)
+        if n < 0:
+            _check(int(n))
+        self.Hkv, self.d, self.capacity, self.S = Hkv, d, capacity, n_streams
+        self.data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+        self._dev = self.data.get_device()
+
+    def _tokens(self, t, heads, name, dtype, n=None):
+        """Checks a [(S,) n, heads, d] tensor; returns its n."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        lead = (self.S,) if t.dim() == 4 or self.S != 1 else ()
+        if n is None:
+            n = t.shape[-3] if t.dim() >= 3 else 0
+        _need(t, lead + (n, heads, self.d), dtype, name)
+        self._same_device(t, name)
+        return n
+
+    def _same_device(self, t, name):
+        if t.get_device() != self._dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.data.device}")
+
+    def _at(self, at, name):
+        """(host value, device pointer) of a token number or an int32 [S] tensor."""
+        if isinstance(at, torch.Tensor):
+            _need(at, (self.S,), torch.int32, name)
+            self._same_device(at, name)
+            return 0, at.data_ptr()
+        return int(at), None
+
+    def append(self, k, v, start, stream=None):
+        """Quantise k, v [(S,) n, Hkv, d] into cache tokens start .. start+n-1
+        (start: a number, or int32 [S] on the device for a start per stream,
+        where tokens outside the cache are dropped)."""
+        code = _dtype_code(k.dtype)
+        n = self._tokens(k, self.Hkv, "k", k.dtype)
+        _need(v, k.shape, k.dtype, "v")
+        self._same_device(v, "v")
+        host, dev = self._at(start, "start")
+        with _device(self._dev):
+            _check(lib.statekv_q4_append(self.data.data_ptr(), self.S, self.Hkv, self.d, self.capacity,
+                                         k.data_ptr(), v.data_ptr(), n, code, host, dev,
+                                         _stream_ptr(stream, self._dev)))
+
+    def read(self, start, n, dtype="bf16", k=None, v=None, stream=None):
+        """Keys and values [S][n][Hkv][d] of cache tokens start .. start+n-1
+        (start as in append; rows of tokens outside the cache are left as they
+        were, and are unset in tensors that this call creates)."""
+        code = _dtype_code(dtype)
+        dt = _torch_dtype(code)
+        shape = (self.S, n, self.Hkv, self.d)
+        host, dev = self._at(start, "start")
+        made = []
+        for i, t in enumerate((k, v)):
+            if t is None:
+                t = _empty(shape, dt, self.data.device, stream)
+            else:
+                _need(t, shape, dt, "kv"[i])
+                self._same_device(t, "kv"[i])
+            made.append(t)
+        with _device(self._dev):
+            _check(lib.statekv_q4_read(self.data.data_ptr(), self.S, self.Hkv, self.d, self.capacity, host, dev, n,
+                                       code, made[0].data_ptr(), made[1].data_ptr(), _stream_ptr(stream, self._dev)))
+        return made[0], made[1]
+
+    def decode(self, q, k, v, length, window=0, n_sink=0, out=None, lse=None, with_lse=True, stream=None):
+        """Attention of n text tokens over the first `length` cache tokens (a
+        number, or int32 [S] on the device) and causally over themselves:
+        q [(S,) n, Hq, d], k/v [(S,) n, Hkv, d]; with window > 0 a token at
+        position p sees positions above p - window and those below n_sink.
+        Returns (out, lse [(S,) Hq, n] or None)."""
+        code = _dtype_code(q.dtype)
+        Hq = q.shape[-2]
+        n = self._tokens(q, Hq, "q", q.dtype)
+        self._tokens(k, self.Hkv, "k", q.dtype, n)
+        self._tokens(v, self.Hkv, "v", q.dtype, n)
+        host, dev = self._at(length, "length")
+        if out is None:
+            out = _empty(q.shape, q.dtype, q.device, stream)
+        else:
+            _need(out, q.shape, q.dtype, "out")
+            self._same_device(out, "out")
+        ls = ((self.S,) if q.dim() == 4 else ()) + (Hq, n)
+        if lse is not None:
+            _need(lse, ls, torch.float32, "lse")
+            self._same_device(lse, "lse")
+        elif with_lse:
+            lse = _empty(ls, torch.float32, q.device, stream)
+        with _device(self._dev):
+            _check(lib.statekv_q4_decode(self.data.data_ptr(), self.S, Hq, self.Hkv, self.d, self.capacity,
+                                         q.data_ptr(), k.data_ptr(), v.data_ptr(), n, code, host, dev, window, n_sink,
+                                         out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                         _stream_ptr(stream, self._dev)))
+        return out, lse
+
+
+def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=True, stream=None):
+    """Causal attention with a sliding window and n_sink first tokens that stay
+    visible, over q [(S,) N, Hq, d], k/v [(S,) N, Hkv, d]: token i sees j <= i
+    with j > i - window or j < n_sink.  Returns (out, lse [(S,) Hq, N] or None)."""
+    batched = q.dim() == 4
+    S = q.shape[0] if batched else 1
+    N, Hq, d = q.shape[-3:]
+    Hkv = k.shape[-2]
+    code = _dtype_code(q.dtype)
+    lead = (S,) if batched else ()
+    _need(q, lead + (N, Hq, d), q.dtype, "q")
+    _need(k, lead + (N, Hkv, d), q.dtype, "k")
+    _need(v, lead + (N, Hkv, d), q.dtype, "v")
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    _need(out, lead + (N, Hq, d), q.dtype, "out")
+    if lse is None and with_lse:
+        lse = _empty(lead + (Hq, N), torch.float32, q.device, stream)
+    if lse is not None:
+        _need(lse, lead + (Hq, N), torch.float32, "lse")
+    dev = q.get_device()
+    for t, name in ((k, "k"), (v, "v"), (out, "out"), (lse, "lse")):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    with _device(dev):
+        _check(lib.sink_window_prefill_batched(q.data_ptr(), k.data_ptr(), v.data_ptr(), S, N, Hq, Hkv, d, code,
+                                               window, n_sink, out.data_ptr(),
+                                               lse.data_ptr() if lse is not None else None, _stream_ptr(stream, dev)))
     return out, lse

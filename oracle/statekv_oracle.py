@@ -380,3 +380,76 @@ def causal_attention_rows(q, k, v, rows):
             out[r, h] = o[0]
             lse[h, r] = l[0]
     return out, lse
+
+
+# ------------------------------------------------- 4-bit cache and sink window
+
+
+def bf16_grid(x, up: bool) -> np.ndarray:
+    """x rounded to a bfloat16 value (8 significant bits, exponents down to
+    2^-126, subnormals in steps of 2^-133), upwards or downwards."""
+    x = np.asarray(x, dtype=np.float64)
+    _, e = np.frexp(x)                      # |x| = f * 2^e, f in [1/2, 1)
+    step = np.ldexp(1.0, np.maximum(np.where(x == 0, -133, e - 8), -133))
+    return (np.ceil if up else np.floor)(x / step) * step
+
+
+def q4_codes(x, group: int = 64):
+    """(codes, s, m) of x [..., d]: per group of `group` channels m = the
+    smallest value rounded down to bfloat16, s = (largest - m) / 15 rounded up,
+    code = the integer nearest to (x - m) / s (ties to even; 0 where s = 0)."""
+    x = to_f64(x)
+    xg = x.reshape(x.shape[:-1] + (x.shape[-1] // group, group))
+    m = bf16_grid(xg.min(-1), up=False)
+    s = bf16_grid((xg.max(-1) - m) / 15.0, up=True)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        c = np.where(s[..., None] > 0, np.rint((xg - m[..., None]) / s[..., None]), 0.0)
+    return c, s, m
+
+
+def q4_held(x, group: int = 64) -> np.ndarray:
+    """The values that a 4-bit cache holds for x [..., d]: m + c * s.  A group
+    with a NaN or an infinity holds NaN."""
+    with np.errstate(invalid="ignore"):
+        c, s, m = q4_codes(x, group)
+        held = m[..., None] + c * s[..., None]
+    xg = to_f64(x).reshape(held.shape)
+    held = np.where(np.isfinite(xg).all(-1, keepdims=True), held, np.nan)
+    return held.reshape(held.shape[:-2] + (-1,))
+
+
+def window_attention(q, k, v, past_k=None, past_v=None, window: int = 0, n_sink: int = 0):
+    """Causal attention of n tokens that follow L past tokens, with a sliding
+    window and visible first tokens.
+
+    q [n][Hq][d], k/v [n][Hkv][d], past_k/past_v [L][Hkv][d] or None.  Token i
+    stands at position L + i and sees position p <= L + i if window is 0, if
+    p > L + i - window or if p < n_sink.  Hidden keys and values take no part.
+    Returns (out [n][Hq][d], lse [Hq][n] natural log, mass [n][Hq][d] = the
+    attention's weights times |v|, span [Hq][n] = the largest sum |q||k| /
+    sqrt(d) over the keys a token sees: the sizes that rounding errors scale
+    with)."""
+    q, k, v = to_f64(q), to_f64(k), to_f64(v)
+    if past_k is not None:
+        k = np.concatenate([to_f64(past_k), k])
+        v = np.concatenate([to_f64(past_v), v])
+    n, Hq, d = q.shape
+    L, Hkv = k.shape[0] - n, k.shape[1]
+    pos = np.arange(L + n)
+    out, mass = np.empty((n, Hq, d)), np.empty((n, Hq, d))
+    lse, span = np.empty((Hq, n)), np.empty((Hq, n))
+    for i in range(n):
+        see = pos <= L + i
+        if window:
+            see &= (pos > L + i - window) | (pos < n_sink)
+        for h in range(Hq):
+            g = kv_head_of(h, Hq, Hkv)
+            kk, vv = k[see, g], v[see, g]
+            a = kk @ q[i, h] / np.sqrt(d)
+            top = a.max()
+            w = np.exp(a - top)
+            lse[h, i] = top + np.log(w.sum())
+            w /= w.sum()
+            out[i, h], mass[i, h] = w @ vv, w @ np.abs(vv)
+            span[h, i] = (np.abs(kk) @ np.abs(q[i, h])).max() / np.sqrt(d)
+    return out, lse, mass, span
