@@ -360,11 +360,18 @@ int statekv_q4_read(const void* cache, int n_streams, int Hkv, int d, int capaci
  * above L + i - window and those below n_sink (window = 0: no window, n_sink
  * unused).  Scale 1/sqrt(d).  A key or value the mask hides has no influence,
  * whatever it holds.  The text tokens are not written to the cache.
+ * workspace: device memory of at least statekv_q4_decode_workspace bytes
+ * (16-byte aligned) that no other work uses until this call's has run; its
+ * contents do not matter.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int statekv_q4_decode(const void* cache, int n_streams, int Hq, int Hkv, int d, int capacity,
                       const void* q, const void* k, const void* v, int n_text, int dtype,
                       int length, const int32_t* lengths, int window, int n_sink, void* out,
-                      float* lse, void* stream);
+                      float* lse, void* workspace, long long workspace_bytes, void* stream);
+
+/* Workspace bytes of statekv_q4_decode on the current device; negative
+ * statekv_status on a bad shape. */
+long long statekv_q4_decode_workspace(int n_streams, int Hq, int Hkv, int d, int n_text, int dtype);
 
 /* Causal self-attention over n_tokens tokens with a sliding window and first
  * tokens that stay visible: token i attends to the tokens j <= i with

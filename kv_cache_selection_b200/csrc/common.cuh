@@ -157,6 +157,14 @@ struct WindowArgs {
   float scale_log2;          // log2(e)/sqrt(d)
 };
 
+// Attention over the 4-bit cache in W workers per tile of query rows.
+struct Q4AttnArgs {
+  WindowArgs w;
+  float* part_o;             // [row tiles][W + S * Hkv][rows][d] unnormalised O
+  float* part_ml;            // [row tiles][W + S * Hkv][rows][2] log2 maximum, sum
+  int W, rows;               // workers; query rows per tile
+};
+
 // Cached tokens of stream s, clipped to the cache.
 __device__ __forceinline__ int q4_length(const WindowArgs& a, int s) {
   const int L = a.lengths ? __ldg(a.lengths + s) : a.length;

@@ -114,6 +114,13 @@ MergeArgs merge_args(const AttnTcArgs& a, int d);
 // a sequence alone) on the CUDA cores.
 cudaError_t launch_q4_append(Q4IoArgs a, int dtype, int d, cudaStream_t st, bool pdl = false);
 cudaError_t launch_q4_read(Q4IoArgs a, int dtype, int d, cudaStream_t st);
+// Attention over the cache: how a call is split, and the bytes of its workspace.
+struct Q4Plan {
+  int rows, n_rb, W;       // query rows per tile, tiles, workers per tile
+  size_t o_bytes, bytes;
+};
+Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm);
+cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st);
 cudaError_t launch_window_simt(const WindowArgs& a, int dtype, int d, cudaStream_t st);
 
 // Message for statekv_last_error(NULL) (errors of calls without a handle).

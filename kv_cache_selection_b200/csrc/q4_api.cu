@@ -65,6 +65,30 @@ size_t cache_bytes(int S, int Hkv, int d, int capacity) {
   return (size_t)S * Hkv * (((size_t)capacity + 31) / 32) * skv::q4_block_bytes(d);
 }
 
+int sm_count() {
+  static int cached[64];  // a device's SM count does not change
+  int dev = 0, n = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return n;
+  }
+  if (cached[dev]) return cached[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) cached[dev] = n;
+  return n;
+}
+
+// Shapes of a decode over a cache.
+int check_decode_shape(int S, int Hq, int Hkv, int d, int capacity, int n_text, int dtype) {
+  int rc;
+  if ((rc = check_cache_shape(S, Hkv, d, capacity)) || (rc = check_dtype(dtype))) return rc;
+  if (Hq < 1 || Hq % Hkv) return fail(STATEKV_ERR_INVALID_ARG, "Hq (%d) %% Hkv (%d) != 0", Hq, Hkv);
+  if (n_text < 1) return fail(STATEKV_ERR_INVALID_ARG, "n_text=%d must be >= 1", n_text);
+  if (Hq > 65535 || n_text > 65535 || (long long)(Hq / Hkv) * n_text > 65535 * 8ll ||
+      (long long)S * Hq * n_text > 0x7fffffffll)
+    return fail(STATEKV_ERR_UNSUPPORTED, "n_streams=%d x Hq=%d x n_text=%d is too large", S, Hq, n_text);
+  return STATEKV_OK;
+}
+
 // A range of n tokens from `start` (host value, or per stream from the device).
 int check_range(int start, const int32_t* starts, int n, int capacity) {
   if (n < 0) return fail(STATEKV_ERR_INVALID_ARG, "negative token count %d", n);
@@ -146,27 +170,35 @@ int statekv_q4_read(const void* cache, int n_streams, int Hkv, int d, int capaci
   return STATEKV_OK;
 }
 
+long long statekv_q4_decode_workspace(int n_streams, int Hq, int Hkv, int d, int n_text, int dtype) {
+  const int rc = check_decode_shape(n_streams, Hq, Hkv, d, 1, n_text, dtype);
+  return rc ? rc : (long long)skv::q4_plan(n_streams, Hq, Hkv, n_text, dtype, d, sm_count()).bytes;
+}
+
 int statekv_q4_decode(const void* cache, int n_streams, int Hq, int Hkv, int d, int capacity, const void* q,
                       const void* k, const void* v, int n_text, int dtype, int length, const int32_t* lengths,
-                      int window, int n_sink, void* out, float* lse, void* stream) {
+                      int window, int n_sink, void* out, float* lse, void* workspace, long long workspace_bytes,
+                      void* stream) {
   int rc;
-  if ((rc = check_cache_shape(n_streams, Hkv, d, capacity)) || (rc = check_dtype(dtype))) return rc;
-  if (Hq < 1 || Hq % Hkv) return fail(STATEKV_ERR_INVALID_ARG, "Hq (%d) %% Hkv (%d) != 0", Hq, Hkv);
-  if (Hq > 65535) return fail(STATEKV_ERR_UNSUPPORTED, "Hq=%d above 65535", Hq);
-  if (n_text < 1) return fail(STATEKV_ERR_INVALID_ARG, "n_text=%d must be >= 1", n_text);
-  if (n_text > (1 << 20)) return fail(STATEKV_ERR_UNSUPPORTED, "n_text=%d above 2^20", n_text);
+  if ((rc = check_decode_shape(n_streams, Hq, Hkv, d, capacity, n_text, dtype))) return rc;
   if (window < 0 || n_sink < 0)
     return fail(STATEKV_ERR_INVALID_ARG, "window=%d and n_sink=%d must not be negative", window, n_sink);
   if (!lengths && (length < 0 || length > capacity))
     return fail(STATEKV_ERR_INVALID_ARG, "length=%d outside [0, capacity=%d]", length, capacity);
-  if (!cache || !q || !k || !v || !out) return fail(STATEKV_ERR_INVALID_ARG, "null input/output pointer");
+  if (!cache || !q || !k || !v || !out || !workspace)
+    return fail(STATEKV_ERR_INVALID_ARG, "null input, output or workspace pointer");
+  if (misaligned(workspace, 16)) return fail(STATEKV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  const skv::Q4Plan pl = skv::q4_plan(n_streams, Hq, Hkv, n_text, dtype, d, sm_count());
+  if (workspace_bytes < (long long)pl.bytes)
+    return fail(STATEKV_ERR_INVALID_ARG, "workspace of %lld bytes, %zu needed", workspace_bytes, pl.bytes);
   if (misaligned(cache, 16) || misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16))
     return fail(STATEKV_ERR_INVALID_ARG, "cache/q/k/v/out must be 16-byte aligned");
   if (misaligned(lse, 4) || misaligned(lengths, 4))
     return fail(STATEKV_ERR_INVALID_ARG, "lse and lengths must be 4-byte aligned");
   const size_t es = dtype == STATEKV_BF16 ? 2 : 4;
   const size_t qb = (size_t)n_streams * n_text * Hq * d * es, kb = (size_t)n_streams * n_text * Hkv * d * es;
-  const Range outs[] = {{out, qb, "out"}, {lse, (size_t)n_streams * Hq * n_text * 4, "lse"}};
+  const Range outs[] = {{out, qb, "out"}, {lse, (size_t)n_streams * Hq * n_text * 4, "lse"},
+                        {workspace, pl.bytes, "workspace"}};
   const Range ins[] = {{cache, cache_bytes(n_streams, Hkv, d, capacity), "cache"}, {q, qb, "q"}, {k, kb, "k"},
                        {v, kb, "v"}, {lengths, (size_t)n_streams * 4, "lengths"}};
   if ((rc = check_disjoint(outs, ins))) return rc;
@@ -188,7 +220,7 @@ int statekv_q4_decode(const void* cache, int n_streams, int Hq, int Hkv, int d, 
   a.window = window;
   a.n_sink = n_sink;
   a.scale_log2 = skv::kLog2e / sqrtf((float)d);
-  const cudaError_t e = skv::launch_window_simt(a, dtype, d, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = skv::launch_q4_attn(a, pl, workspace, dtype, d, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(STATEKV_ERR_CUDA, "q4 decode launch failed: %s", cudaGetErrorString(e));
   return STATEKV_OK;
 }

@@ -1,0 +1,676 @@
+// Attention of a few text tokens over the 4-bit cache (format: q4_cache.cuh),
+// streamed once, codes fed to the tensor cores without being dequantised.
+//
+// With codes c, scales s and smallest values m per (token j, group g):
+//   q . k_j  = sum_g [ s_jg (q_g . c_jg) + m_jg sum(q_g) ],
+//   O        = sum_j p_j v_j = sum_j (p_j s_jg) (c_jg - 8) + sum_j p_j (m_jg + 8 s_jg).
+// The codes are exact fp16 numbers (one shift and one and-or give a pair of
+// 16 + c), so both sums are fp16 products with float32 accumulation, and the
+// scales meet float32 numbers only.  The rows are the G query heads of a KV
+// head times the text tokens, eight to a tile.
+//   Q: scaled by a power of two per row (largest element in [2^10, 2^11)); bf16
+//     values are then exact in fp16, float32 ones are split into two fp16 parts
+//     (NS = 2), 22 bits.
+//   P s: in fp16 relative to the largest V scale met so far (a power of two
+//     R_g per group, lazily raised as the row maximum is): 2^-11 off at most,
+//     an eighth of what the bf16 result rounds by; float32 again takes two parts.
+//   P: relative to a row maximum that moves only when a logit exceeds it by
+//     more than 2^8, so that most blocks need one vote and no shuffle.
+// Tensor-core shape m16n8k16 with tokens (K) or channels (V) as the 16 rows and
+// query rows as the 8 columns: the fragments come from shared memory as stored,
+// S^T turns into P^T's fragment by an 8x8 transpose, and nothing but 4-bit codes
+// is staged.  A tcgen05 product would need the tile dequantised into shared
+// memory first, 4x the bytes per value, for rows that fill 8 of its 128.
+//
+// The visible 32-token blocks of all (stream, KV head) are numbered in order
+// and dealt evenly to the W workers (thread blocks), so ragged streams balance;
+// a worker writes one partial (max, sum, O) per (stream, KV head) it meets, and
+// q4_merge_kernel joins them in worker order with the text tokens' own part.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "q4_cache.cuh"
+#include "tc_common.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kWarps = 12;
+constexpr int kStages = 4;      // blocks in flight per warp
+constexpr float kRaise = 8.f;   // log2 headroom of the lazy row maximum
+constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
+constexpr float kPScale = 64.f; // P s <= 2^8 * 64 < 65504
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ float2 unpack_half2(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
+
+// A pair of codes as fp16: 16 + c, or c - 8.
+template <int F>
+__device__ __forceinline__ uint32_t code_raw(uint32_t x) {
+  return q4_field<F>(x) | 0x4C004C00u;
+}
+template <int F>
+__device__ __forceinline__ uint32_t code_centred(uint32_t x) {
+  const uint32_t r = code_raw<F>(x);
+  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&r), __half2half2(__ushort_as_half(0x4E00))));  // 24
+}
+
+// Blocks of a stream that any row sees: [0, sinks) and [window, n).
+struct Visible {
+  int L, sinks, window, n;
+  __device__ __forceinline__ int count() const { return sinks + n - window; }
+  __device__ __forceinline__ int block(int v) const { return v < sinks ? v : v - sinks + window; }
+};
+__device__ __forceinline__ Visible visible_of(const WindowArgs& a, int s) {
+  Visible x;
+  x.L = q4_length(a, s);
+  x.n = (x.L + kQ4Tokens - 1) / kQ4Tokens;
+  x.sinks = 0;
+  x.window = 0;
+  if (a.window) {
+    x.sinks = (min(a.n_sink, x.L) + kQ4Tokens - 1) / kQ4Tokens;
+    const long long lo = (long long)x.L - a.window + 1;  // first token of row 0's window
+    x.window = lo >= x.L ? x.n : lo > 0 ? (int)(lo / kQ4Tokens) : 0;
+    x.window = max(x.window, x.sinks);
+  }
+  return x;
+}
+
+// The numbering of the visible blocks: of (s, g), first block and count; and
+// the worker that owns a block.
+struct Deal {
+  long long total;
+  int W;
+  __device__ __forceinline__ long long first(int w) const { return total * w / W; }
+  __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / total); }
+};
+__device__ __forceinline__ Deal deal_of(const WindowArgs& a, int W) {
+  Deal d;
+  d.W = W;
+  d.total = 0;
+  if (a.lengths) {
+    for (int s = 0; s < a.S; ++s) d.total += visible_of(a, s).count();
+  } else {
+    d.total = (long long)a.S * visible_of(a, 0).count();
+  }
+  d.total *= a.Hkv;
+  if (d.total < W) d.W = (int)d.total;  // every worker that counts owns a block
+  return d;
+}
+
+template <typename T, int D, int NT, int NS>
+__global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
+  using B = Q4Block<D>;
+  constexpr int NG = B::kGroups;
+  constexpr int KW = D / 32;          // K words per (token row, tig)
+  constexpr int MT = D / 16;          // 16-channel tiles of O
+  constexpr int kRows = 8 * NT;
+  constexpr int kStride = D + 4;      // padded row of the partials in shared memory
+  extern __shared__ __align__(16) uint8_t smem[];
+  const WindowArgs& a = p.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int G = a.Hq / a.Hkv, R = G * a.n;
+  const int row0 = blockIdx.y * kRows;
+  uint8_t* ring = smem + warp * (kStages * B::kBytes);
+  const uint32_t ring_u32 = tc::smem_u32(ring);
+
+  pdl_wait();
+  pdl_trigger();
+  const Deal deal = deal_of(a, p.W);
+  if ((int)blockIdx.x >= deal.W) return;
+  long long x = deal.first(blockIdx.x);
+  const long long x_end = deal.first(blockIdx.x + 1);
+  int s = 0;
+  long long s_base = 0;
+  Visible vis = visible_of(a, 0);
+  // text tokens of the tile's rows (rows behind R take the last one)
+  const int i_first = row0 / G, i_last = (min(row0 + kRows, R) - 1) / G;
+
+  while (x < x_end) {
+    while (x >= s_base + (long long)a.Hkv * vis.count()) {
+      s_base += (long long)a.Hkv * vis.count();
+      vis = visible_of(a, ++s);
+    }
+    const int g = (int)((x - s_base) / vis.count());
+    const int v0 = (int)((x - s_base) % vis.count());
+    const int v1 = (int)min((long long)vis.count(), v0 + (x_end - x));
+    const uint8_t* base = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
+
+    auto issue = [&](int v, int stage) {
+      if (v < v1) {
+        const uint8_t* src = base + (long long)vis.block(v) * B::kBytes;
+        const uint32_t dst = ring_u32 + stage * B::kBytes;
+#pragma unroll
+        for (int c = 0; c < (B::kBytes / 16 + 31) / 32; ++c)
+          if ((c + 1) * 32 <= B::kBytes / 16 || c * 32 + lane < B::kBytes / 16)
+            cp16(dst + (c * 32 + lane) * 16, src + (c * 32 + lane) * 16);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int st = 0; st < kStages; ++st) issue(v0 + warp + st * kWarps, st);
+
+    // ---- Q fragments, per-row scale and group sums
+    uint32_t qf[NT][NS][MT][2];
+    float qsum[NT][NG][2], rs[NT][2];
+    int irow[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + gid;
+      float qv[KW][8];
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qv[w][e] = 0.f;
+      if (r < R) {
+        const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + r / G) * a.Hq + g * G + r % G) * D;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qv[w][e] = to_f(q[(w >> 1) * 64 + tig * 16 + (w & 1) * 8 + e]);
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(qv[w][e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // largest element into [2^10, 2^11); 1 for a zero row or one with an infinity
+      int ex = (int)(__float_as_uint(top) >> 23);
+      ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, 12);
+      const float up = __uint_as_float((uint32_t)(264 - ex) << 23);  // 2^(10 - (ex - 127))
+      const float down = __uint_as_float((uint32_t)(ex - 10) << 23);
+      float sum[NG];
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg) sum[gg] = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float x0 = qv[w][2 * f] * up, x1 = qv[w][2 * f + 1] * up;
+          const __half2 hi = __floats2half2_rn(x0, x1);
+          const float2 h = __half22float2(hi);
+          qf[nt][0][2 * w + (f >> 1)][f & 1] = half2_bits(hi);
+          if (NS == 2) {
+            qf[nt][NS - 1][2 * w + (f >> 1)][f & 1] = half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y));
+            sum[w >> 1] += x0 + x1;
+          } else {
+            sum[w >> 1] += h.x + h.y;
+          }
+        }
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg) {
+        sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 1);
+        sum[gg] += __shfl_xor_sync(0xffffffffu, sum[gg], 2);
+      }
+      // this lane's columns of S^T are rows 2 tig and 2 tig + 1 of the tile
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int from = (2 * tig + e) * 4;
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) qsum[nt][gg][e] = __shfl_sync(0xffffffffu, sum[gg], from);
+        rs[nt][e] = __shfl_sync(0xffffffffu, down, from) * a.scale_log2;
+        irow[nt][e] = min(row0 + nt * 8 + 2 * tig + e, R - 1) / G;
+      }
+    }
+
+    float o[NT][MT][4], corr[NT][NG][2], l[NT][2], m[NT][2], vR[NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] = 0.f;
+        m[nt][e] = -INFINITY;
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int gg = 0; gg < NG; ++gg) vR[gg] = kMinR;
+
+    int stage = 0;
+    for (int v = v0 + warp; v < v1; v += kWarps) {
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* blk = ring + stage * B::kBytes;
+      const int t0 = vis.block(v) * kQ4Tokens;
+      bool full = t0 + kQ4Tokens <= vis.L;
+      if (a.window)
+        full = full && ((long long)t0 > (long long)vis.L + i_last - a.window || t0 + kQ4Tokens <= a.n_sink);
+      // ---- S^T = K Q^T, 16 tokens at a time; t = logits in log2 units
+      float t[NT][2][4];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        uint32_t ka[KW], kb[KW];
+        const uint8_t* kr = blk + (kt * 16 + gid) * B::kRow + tig * (D / 8);
+        if (D == 128) {
+          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(kr);
+          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(kr + 8 * B::kRow);
+        } else {
+          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(kr);
+          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kr + 8 * B::kRow);
+        }
+        float acc[NT][NG][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nt][gg][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t f[8];
+          if (NS == 2) {
+            f[0] = code_centred<0>(ka[w]), f[1] = code_centred<0>(kb[w]);
+            f[2] = code_centred<1>(ka[w]), f[3] = code_centred<1>(kb[w]);
+            f[4] = code_centred<2>(ka[w]), f[5] = code_centred<2>(kb[w]);
+            f[6] = code_centred<3>(ka[w]), f[7] = code_centred<3>(kb[w]);
+          } else {
+            f[0] = code_raw<0>(ka[w]), f[1] = code_raw<0>(kb[w]);
+            f[2] = code_raw<1>(ka[w]), f[3] = code_raw<1>(kb[w]);
+            f[4] = code_raw<2>(ka[w]), f[5] = code_raw<2>(kb[w]);
+            f[6] = code_raw<3>(ka[w]), f[7] = code_raw<3>(kb[w]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns) {
+              mma16816(acc[nt][w >> 1], f[0], f[1], f[2], f[3], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
+              mma16816(acc[nt][w >> 1], f[4], f[5], f[6], f[7], qf[nt][ns][2 * w + 1][0], qf[nt][ns][2 * w + 1][1]);
+            }
+        }
+        const uint32_t* ks = reinterpret_cast<const uint32_t*>(blk + B::kKs) + (kt * 16 + gid) * NG;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) {
+            const uint32_t sm = ks[hh * 8 * NG + gg];
+            const float sc = q4_scale(sm), mid = fmaf(sc, NS == 2 ? 8.f : -16.f, q4_min(sm));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float part = fmaf(sc, acc[nt][gg][hh * 2 + e], mid * qsum[nt][gg][e]);
+                t[nt][kt][hh * 2 + e] = gg == 0 ? part : t[nt][kt][hh * 2 + e] + part;
+              }
+          }
+      }
+      // ---- V scales of this lane's tokens (t0 + 16 kt + 8 hh + gid)
+      float sv[2][2][NG], mv[2][2][NG];
+      const uint32_t* vsp = reinterpret_cast<const uint32_t*>(blk + B::kVs);
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) {
+            const uint32_t sm = vsp[(kt * 16 + hh * 8 + gid) * NG + gg];
+            sv[kt][hh][gg] = q4_scale(sm);
+            mv[kt][hh][gg] = fmaf(sv[kt][hh][gg], 8.f, q4_min(sm));
+          }
+      // ---- masks: hidden tokens get a logit of -inf; a V scale no row uses gets 0
+      uint32_t seen = 0xffffffffu;  // bit nt*8 + kt*4 + hh*2 + e
+      if (!full) {
+        seen = 0;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int tok = t0 + kt * 16 + hh * 8 + gid;
+            const bool in = tok < vis.L;
+            const bool keep = !a.window || tok < a.n_sink;
+            if (!(in && (keep || (long long)tok > (long long)vis.L + i_first - a.window))) {
+#pragma unroll
+              for (int gg = 0; gg < NG; ++gg) sv[kt][hh][gg] = mv[kt][hh][gg] = 0.f;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const bool ok = in && (keep || (long long)tok > (long long)vis.L + irow[nt][e] - a.window);
+                if (ok) seen |= 1u << (nt * 8 + kt * 4 + hh * 2 + e);
+                else t[nt][kt][hh * 2 + e] = -INFINITY;
+              }
+          }
+      }
+      // ---- lazy row maximum and V reference
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float& x_ = t[nt][c >> 1][(c & 1) * 2 + e];
+            x_ *= rs[nt][e];
+            raise |= x_ > m[nt][e] + kRaise;
+          }
+        }
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg)
+        raise |= fmaxf(fmaxf(sv[0][0][gg], sv[0][1][gg]), fmaxf(sv[1][0][gg], sv[1][1][gg])) > vR[gg];
+      if (__any_sync(0xffffffffu, raise)) {
+        float fo[NT][2], fv[NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(fmaxf(t[nt][0][e], t[nt][0][2 + e]), fmaxf(t[nt][1][e], t[nt][1][2 + e]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float nm = fmaxf(m[nt][e], top);
+            fo[nt][e] = nm == m[nt][e] ? 1.f : tc::ex2_approx(m[nt][e] - nm);
+            m[nt][e] = nm;
+            l[nt][e] *= fo[nt][e];
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] *= fo[nt][e];
+          }
+#pragma unroll
+        for (int gg = 0; gg < NG; ++gg) {
+          float top = fmaxf(fmaxf(sv[0][0][gg], sv[0][1][gg]), fmaxf(sv[1][0][gg], sv[1][1][gg]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float up = __uint_as_float((__float_as_uint(top) + 0x7fffffu) & 0x7f800000u);  // next power of two
+          const float nr = fmaxf(vR[gg], up);
+          fv[gg] = vR[gg] / nr;
+          vR[gg] = nr;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][mt][e] *= fo[nt][e & 1] * fv[mt / 4];
+      }
+      // ---- P, its sums, and P s as fp16 fragments
+      uint32_t pf[NT][NS][NG][2][2];
+      float vs[NG];
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg) vs[gg] = kPScale / vR[gg];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float p0 = tc::ex2_approx(t[nt][kt][hh * 2] - m0), p1 = tc::ex2_approx(t[nt][kt][hh * 2 + 1] - m1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            const bool ok0 = seen >> (nt * 8 + kt * 4 + hh * 2) & 1, ok1 = seen >> (nt * 8 + kt * 4 + hh * 2 + 1) & 1;
+#pragma unroll
+            for (int gg = 0; gg < NG; ++gg) {
+              const float sc = sv[kt][hh][gg] * vs[gg];
+              float x0 = p0 * sc, x1 = p1 * sc, y0 = p0 * mv[kt][hh][gg], y1 = p1 * mv[kt][hh][gg];
+              if (!full) {  // a hidden token's scale may be NaN
+                if (!ok0) x0 = y0 = 0.f;
+                if (!ok1) x1 = y1 = 0.f;
+              }
+              corr[nt][gg][0] += y0;
+              corr[nt][gg][1] += y1;
+              const __half2 hi = __floats2half2_rn(x0, x1);
+              pf[nt][0][gg][kt][hh] = transpose8x8(half2_bits(hi));
+              if (NS == 2) {
+                const float2 h = __half22float2(hi);
+                pf[nt][NS - 1][gg][kt][hh] = transpose8x8(half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y)));
+              }
+            }
+          }
+      }
+      // ---- O^T += V^T P^T, 32 channels at a time
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(blk + B::kV + c * 512 + lane * 16);
+        const int gg = c / 2;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t x0 = half ? w.z : w.x, x1 = half ? w.w : w.y;
+          uint32_t f[8];
+          f[0] = code_centred<0>(x0), f[1] = code_centred<0>(x1), f[2] = code_centred<1>(x0), f[3] = code_centred<1>(x1);
+          f[4] = code_centred<2>(x0), f[5] = code_centred<2>(x1), f[6] = code_centred<3>(x0), f[7] = code_centred<3>(x1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ns = 0; ns < NS; ++ns) {
+              mma16816(o[nt][2 * c + half], f[0], f[1], f[2], f[3], pf[nt][ns][gg][0][0], pf[nt][ns][gg][0][1]);
+              mma16816(o[nt][2 * c + half], f[4], f[5], f[6], f[7], pf[nt][ns][gg][1][0], pf[nt][ns][gg][1][1]);
+            }
+        }
+      }
+      __syncwarp();
+      issue(v + kStages * kWarps, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+
+    // ---- the warps' results into shared memory (over the drained ring)
+    __syncthreads();
+    float* wo = reinterpret_cast<float*>(smem);                        // [kWarps][kRows][kStride]
+    float* wml = wo + kWarps * kRows * kStride;                        // [kWarps][kRows][2]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], off);
+#pragma unroll
+          for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] += __shfl_xor_sync(0xffffffffu, corr[nt][gg][e], off);
+        }
+        if (gid == 0) {
+          float* ml = wml + ((warp * kRows) + nt * 8 + 2 * tig + e) * 2;
+          ml[0] = m[nt][e];
+          ml[1] = l[nt][e];
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          wo[(warp * kRows + nt * 8 + 2 * tig + (e & 1)) * kStride + mt * 16 + (e >> 1) * 8 + gid] =
+              fmaf(o[nt][mt][e], vR[mt / 4] * (1.f / kPScale), corr[nt][mt / 4][e & 1]);
+    }
+    __syncthreads();
+    const long long part = (long long)blockIdx.y * (p.W + a.S * a.Hkv) + blockIdx.x + s * a.Hkv + g;
+    for (int e = threadIdx.x; e < kRows * (D / 4); e += kWarps * 32) {
+      const int r = e / (D / 4), c = e % (D / 4);
+      if (row0 + r >= R) break;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wml[(w * kRows + r) * 2]);
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = tc::ex2_approx(wml[(w * kRows + r) * 2] - ref);
+        ls += f * wml[(w * kRows + r) * 2 + 1];
+        const float4 x4 = *reinterpret_cast<const float4*>(wo + (w * kRows + r) * kStride + c * 4);
+        acc.x += f * x4.x;
+        acc.y += f * x4.y;
+        acc.z += f * x4.z;
+        acc.w += f * x4.w;
+      }
+      *reinterpret_cast<float4*>(p.part_o + (part * kRows + r) * D + c * 4) = acc;
+      if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (part * kRows + r) * 2) = make_float2(mx, ls);
+    }
+    __syncthreads();
+    x += v1 - v0;
+  }
+}
+
+// One block per (stream, query head, text token): the workers' partials of its
+// KV head and the visible text tokens, dealt to eight warps, each with its own
+// running maximum; then the eight are joined in order.
+constexpr int kMergeWarps = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p) {
+  constexpr int E = D / 32;  // channels per lane
+  __shared__ float s_acc[kMergeWarps][D];
+  __shared__ float s_ml[kMergeWarps][2];
+  const WindowArgs& a = p.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv;
+  const long long rw = blockIdx.x;
+  const int i = (int)(rw % a.n), h = (int)(rw / a.n % a.Hq), s = (int)(rw / a.n / a.Hq);
+  const int g = h / G, row = i * G + h % G;
+  float acc[E], m = -INFINITY, l = 0.f, qv[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  auto join = [&](float m2, float l2, const float (&v)[E]) {  // acc += v (weights relative to 2^m2)
+    const float nm = fmaxf(m, m2);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    const float f1 = tc::ex2_approx(m - ref), f2 = tc::ex2_approx(m2 - ref);
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + v[e] * f2;
+    m = nm;
+  };
+  // the call's own tokens (inputs of the call: read before the wait)
+  const Visible vis = visible_of(a, s);
+  const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) qv[e] = to_f(q[e]) * a.scale_log2;
+  for (int j = warp; j <= i; j += kMergeWarps) {
+    if (a.window && j <= i - a.window && (long long)vis.L + j >= a.n_sink) continue;
+    const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
+    float t = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      t = fmaf(qv[e], to_f(static_cast<const T*>(a.k)[at + e]), t);
+      v[e] = to_f(static_cast<const T*>(a.v)[at + e]);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (t != t) l = t;  // a NaN logit makes the row NaN
+    join(t, 1.f, v);
+  }
+  pdl_wait();
+  const Deal deal = deal_of(a, p.W);
+  if (vis.count() > 0) {
+    long long base = 0;
+    if (a.lengths) {
+      for (int s2 = 0; s2 < s; ++s2) base += visible_of(a, s2).count();
+    } else {
+      base = (long long)s * vis.count();
+    }
+    base = base * a.Hkv + (long long)g * vis.count();
+    const int w0 = deal.owner(base), w1 = deal.owner(base + vis.count() - 1);
+    const int sg = s * a.Hkv + g;
+    const long long part0 = (long long)(row / p.rows) * (p.W + a.S * a.Hkv) + sg;
+    const int r = row % p.rows;
+    constexpr int kBatch = 4;
+    for (int w = w0 + warp; w <= w1; w += kMergeWarps * kBatch) {
+      float2 ml[kBatch];
+      float v[kBatch][E];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int u = w + b * kMergeWarps;
+        if (u <= w1) {
+          const long long at = (part0 + u) * p.rows + r;
+          ml[b] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
+          const float* src = p.part_o + at * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[b][e] = src[e];
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (w + b * kMergeWarps <= w1) join(ml[b].x, ml[b].y, v[b]);
+    }
+  }
+  if (lane == 0) {
+    s_ml[warp][0] = m;
+    s_ml[warp][1] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  float mx = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, s_ml[w][0]);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) {
+    float sum = 0.f, ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      const float f = tc::ex2_approx(s_ml[w][0] - ref);
+      ls += f * s_ml[w][1];
+      sum += f * s_acc[w][d];
+    }
+    static_cast<T*>(a.out)[(((long long)s * a.n + i) * a.Hq + h) * D + d] = from_f<T>(sum / ls);
+    if (d == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (mx + log2f(ls)) * kLn2;
+  }
+}
+
+template <typename T, int D, int NT, int NS>
+cudaError_t launch(const Q4AttnArgs& p, int n_rb, cudaStream_t st) {
+  using B = Q4Block<D>;
+  constexpr int ring = kWarps * kStages * B::kBytes;
+  constexpr int merge = kWarps * 8 * NT * (D + 4 + 2) * 4;
+  constexpr int smem = ring > merge ? ring : merge;
+  cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(q4_attn_kernel<T, D, NT, NS>, dim3(p.W, n_rb), dim3(kWarps * 32), smem, st, false, p);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)p.w.S * p.w.Hq * p.w.n;
+  return launch_kernel(q4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(kMergeWarps * 32), 0, st, true, p);
+}
+
+}  // namespace
+
+Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm) {
+  Q4Plan pl{};
+  const long long R = (long long)(Hq / Hkv) * n;
+  pl.rows = dtype == kDtypeF32 || R <= 8 ? 8 : 16;
+  pl.n_rb = (int)((R + pl.rows - 1) / pl.rows);
+  pl.W = std::max(1, n_sm / pl.n_rb);
+  const size_t parts = (size_t)pl.n_rb * (pl.W + (size_t)S * Hkv) * pl.rows;
+  pl.o_bytes = parts * d * 4;
+  pl.bytes = pl.o_bytes + parts * 8;
+  return pl;
+}
+
+cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st) {
+  Q4AttnArgs p{};
+  p.w = a;
+  p.W = pl.W;
+  p.rows = pl.rows;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.o_bytes);
+  if (dtype == kDtypeF32) {
+    return d == 128 ? launch<float, 128, 1, 2>(p, pl.n_rb, st) : launch<float, 64, 1, 2>(p, pl.n_rb, st);
+  }
+  if (pl.rows == 8)
+    return d == 128 ? launch<__nv_bfloat16, 128, 1, 1>(p, pl.n_rb, st) : launch<__nv_bfloat16, 64, 1, 1>(p, pl.n_rb, st);
+  return d == 128 ? launch<__nv_bfloat16, 128, 2, 1>(p, pl.n_rb, st) : launch<__nv_bfloat16, 64, 2, 1>(p, pl.n_rb, st);
+}
+
+}  // namespace skv

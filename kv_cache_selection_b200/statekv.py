@@ -61,7 +61,9 @@ _SIGS = {
     "statekv_q4_bytes": (ctypes.c_longlong, [_i, _i, _i, _i]),
     "statekv_q4_append": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp]),
     "statekv_q4_read": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
-    "statekv_q4_decode": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp]),
+    "statekv_q4_decode": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp,
+                               ctypes.c_longlong, _vp]),
+    "statekv_q4_decode_workspace": (ctypes.c_longlong, [_i, _i, _i, _i, _i, _i]),
     "sink_window_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
     "sink_window_prefill_batched": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
 }
@@ -365,6 +367,7 @@ class Q4Cache:
         self.Hkv, self.d, self.capacity, self.S = Hkv, d, capacity, n_streams
         self.data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
         self._dev = self.data.get_device()
+        self._ws_bytes = {}
 
     def _tokens(self, t, heads, name, dtype, n=None):
         """Checks a [(S,) n, heads, d] tensor; returns its n."""
@@ -448,10 +451,17 @@ class Q4Cache:
         elif with_lse:
             lse = _empty(ls, torch.float32, q.device, stream)
         with _device(self._dev):
+            need = self._ws_bytes.get((Hq, n, code))
+            if need is None:
+                need = lib.statekv_q4_decode_workspace(self.S, Hq, self.Hkv, self.d, n, code)
+                if need < 0:
+                    _check(int(need))
+                self._ws_bytes[(Hq, n, code)] = need
+            ws = _empty((need,), torch.uint8, q.device, stream)
             _check(lib.statekv_q4_decode(self.data.data_ptr(), self.S, Hq, self.Hkv, self.d, self.capacity,
                                          q.data_ptr(), k.data_ptr(), v.data_ptr(), n, code, host, dev, window, n_sink,
-                                         out.data_ptr(), lse.data_ptr() if lse is not None else None,
-                                         _stream_ptr(stream, self._dev)))
+                                         out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
+                                         need, _stream_ptr(stream, self._dev)))
         return out, lse
 
 

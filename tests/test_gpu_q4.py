@@ -57,11 +57,13 @@ def check_attention(out, lse, want, dtype, p_step):
     e = 2.0 ** -19 * span                                  # [Hq][n]
     lim = t * np.abs(w_out) + mass * (p_step + 2 * e.T[..., None] + (64 + want.keys / 16) * 2.0 ** -23)
     err = np.abs(O.to_f64(out.cpu()) - w_out)
-    assert np.isfinite(err).all() and (err <= lim).all(), f"out: worst {np.max(err / lim):.3g} of its limit"
+    fine = bool(np.isfinite(err).all() and (err <= lim).all())
+    assert fine, f"out: worst {np.max(err / lim):.3g} of its limit"
     if lse is not None:
         err = np.abs(O.to_f64(lse.cpu()) - w_lse)
         lim = e + 2.0 ** -20 + 2.0 ** -23 * np.abs(w_lse)
-        assert (err <= lim).all(), f"lse: worst {np.max(err / lim):.3g} of its limit"
+        fine = bool((err <= lim).all())
+        assert fine, f"lse: worst {np.max(err / lim):.3g} of its limit"
 
 
 class Want(tuple):

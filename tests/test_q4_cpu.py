@@ -144,19 +144,23 @@ def test_q4_decode_refusals():
     S = _lib()
 
     def f(cache=_p(0), Sn=1, Hq=4, Hkv=2, d=64, cap=100, q=_p(1), k=_p(2), v=_p(3), n=3, dtype=0, length=50,
-          lengths=None, window=0, n_sink=0, out=_p(4), lse=_p(5)):
+          lengths=None, window=0, n_sink=0, out=_p(4), lse=_p(5), ws=_p(8), wb=1 << 28):
         return S.lib.statekv_q4_decode(cache, Sn, Hq, Hkv, d, cap, q, k, v, n, dtype, length, lengths, window, n_sink,
-                                       out, lse, None)
+                                       out, lse, ws, wb, None)
 
     assert f(Hq=3) == -1
     assert f(Hq=0) == -1
     assert f(d=256) == -2
     assert f(n=0) == -1
-    assert f(n=(1 << 20) + 1) == -2
+    assert f(n=65536) == -2
+    need = S.lib.statekv_q4_decode_workspace(1, 4, 2, 64, 3, 0)
+    assert need > 0 and S.lib.statekv_q4_decode_workspace(1, 4, 3, 64, 3, 0) == -1
+    assert f(wb=need - 1) == -1 and b"workspace" in _msg()
+    assert f(ws=_p(4)) == -1 and f(ws=_p(0)) == -1
     assert f(dtype=5) == -1
     assert f(length=101) == -1 and f(length=-1) == -1
     assert f(window=-1) == -1 and f(n_sink=-1) == -1
-    for name in ("cache", "q", "k", "v", "out"):
+    for name in ("cache", "q", "k", "v", "out", "ws"):
         assert f(**{name: None}) == -1
         assert f(**{name: _p(7, 4)}) == -1
     assert f(lse=_p(5, 2)) == -1 and f(lengths=_p(6, 1)) == -1
