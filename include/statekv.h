@@ -380,8 +380,9 @@ long long statekv_q4_decode_workspace(int n_streams, int Hq, int Hkv, int d, int
  *   q [n_tokens][Hq][d], k,v [n_tokens][Hkv][d], out [n_tokens][Hq][d] (device,
  *   dtype); lse [Hq][n_tokens] float32 natural-log (device) or NULL.
  * window >= 1, n_sink >= 0.  Work grows with n_tokens x (window + n_sink).  A
- * key or value the mask hides has no influence, whatever it holds.  No memory
- * is allocated.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * key or value the mask hides takes no part, whatever it holds (a bf16 row that
+ * shares a tile of 128 keys with a hidden NaN or infinity is computed a second
+ * time, slowly, and may differ in its last bits).  No memory is allocated.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int sink_window_prefill(const void* q, const void* k, const void* v, int n_tokens, int Hq, int Hkv,
                         int d, int dtype, int window, int n_sink, void* out, float* lse,
                         void* stream);
@@ -391,6 +392,13 @@ int sink_window_prefill(const void* q, const void* k, const void* v, int n_token
 int sink_window_prefill_batched(const void* q, const void* k, const void* v, int n_seq,
                                 int n_tokens, int Hq, int Hkv, int d, int dtype, int window,
                                 int n_sink, void* out, float* lse, void* stream);
+
+/* Device-side status of the sink_window_prefill calls on the current device:
+ * *code = 0, or the first error a kernel recorded since the last call (a
+ * pipeline wait that exceeded its time limit, as in statekv_device_status; the
+ * results of that call are invalid).  Synchronises the device, then resets the
+ * word. */
+int sink_window_status(int* code);
 
 #ifdef __cplusplus
 }

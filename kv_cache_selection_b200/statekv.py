@@ -65,6 +65,7 @@ _SIGS = {
                                ctypes.c_longlong, _vp]),
     "statekv_q4_decode_workspace": (ctypes.c_longlong, [_i, _i, _i, _i, _i, _i]),
     "sink_window_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "sink_window_status": (_i, [_ip]),
     "sink_window_prefill_batched": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -494,3 +495,11 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
                                                window, n_sink, out.data_ptr(),
                                                lse.data_ptr() if lse is not None else None, _stream_ptr(stream, dev)))
     return out, lse
+
+
+def sink_window_status() -> int:
+    """0, or the first error code that sink_window_prefill's kernels recorded on
+    the current device since the last call (synchronises)."""
+    code = ctypes.c_int()
+    _check(lib.sink_window_status(ctypes.byref(code)))
+    return code.value
