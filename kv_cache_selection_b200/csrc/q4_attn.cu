@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const float x0 = qv[w][2 * f] * up, x1 = qv[w][2 * f + 1] * up;
+          const float x0 = qv[w][q4_k_channel(f, 0)] * up, x1 = qv[w][q4_k_channel(f, 1)] * up;
           const __half2 hi = __floats2half2_rn(x0, x1);
           const float2 h = __half22float2(hi);
           qf[nt][0][2 * w + (f >> 1)][f & 1] = half2_bits(hi);

@@ -12,8 +12,6 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 256;
-
 // Token range [p0, p1) that the call covers in stream s, clipped to the cache.
 struct Span {
   long long start;  // cache token of the call's token 0
@@ -29,95 +27,227 @@ __device__ __forceinline__ Span span_of(const Q4IoArgs& a, int s) {
   return sp;
 }
 
-// The scale of a group: (hi - m) / 15 rounded up to bfloat16.  The float32
-// quotient is off by at most 3 x 2^-24; where that could change the rounding
-// (the quotient on or next to a bfloat16 value, or far from 1) float64 decides.
-__device__ __forceinline__ float round_scale(float hi, float m) {
-  const float q = (hi - m) * (1.f / 15.f);
-  const uint32_t below = __float_as_uint(q * (1.f - 0x1p-21f)) + 0xffffu, above = __float_as_uint(q * (1.f + 0x1p-21f)) + 0xffffu;
-  uint32_t bits = above;
-  if (((below ^ above) & 0xffff0000u) || !(q >= 0x1p-100f && q <= 0x1p100f))
-    bits = __float_as_uint(__double2float_ru(((double)hi - (double)m) / 15.0)) + 0xffffu;
-  return __uint_as_float(bits & 0xffff0000u);
+// min and max that give NaN where an operand is one
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// Codes of one token row held by a warp, E channels per lane; kLanes lanes
-// share a group.  Returns the packed (s, m) of the lane's group.
-//   y = (x - m) * (1/s) in float32 is off by at most 15 x 3 x 2^-24 < 2^-18;
-//   where that could change the nearest integer float64 decides, so the codes
-//   are those of the exact quotient.
-template <int E, int kLanes>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[E], uint32_t (&c)[E]) {
-  float lo = x[0], hi = x[0], big = 0.f;
+// a - b as d + e exactly (e: what the rounding of d lost)
+__device__ __forceinline__ float exact_difference(float a, float b, float& e) {
+  const float d = __fsub_rn(a, b), z = __fsub_rn(d, a);
+  e = __fsub_rn(__fsub_rn(a, __fsub_rn(d, z)), __fadd_rn(b, z));
+  return d;
+}
+
+// The scale of a group: (hi - m) / 15 rounded up to bfloat16.  The bfloat16
+// value nearest to the float32 quotient is the result or its lower neighbour;
+// the sign of 15 s - (hi - m), exact in one fma, tells which (where the
+// difference itself was rounded and the fma gives 0, the rest decides).
+__device__ __forceinline__ float round_scale(float hi, float m) {
+  float rest;
+  const float d = exact_difference(hi, m, rest), q = d * (1.f / 15.f);
+  if (!(q >= 0x1p-100f && q <= 0x1p100f))  // far from 1 (or 0, or NaN): float64
+    return __uint_as_float((__float_as_uint(__double2float_ru(((double)hi - (double)m) / 15.0)) + 0xffffu) & 0xffff0000u);
+  uint32_t bits = (__float_as_uint(q) + 0x8000u) & 0xffff0000u;
+  const float off = fmaf(__uint_as_float(bits), 15.f, -d);
+  if (off < 0.f || (off == 0.f && rest > 0.f)) bits += 0x10000u;
+  return __uint_as_float(bits);
+}
+
+// The integer nearest to (x - m) / s, ties to even, from c at most 1 away: the
+// remainder x - m - c s is exact in float32 (it is at most s and a multiple of
+// the last place of x - m), so its place against s / 2 is, too.
+__device__ __forceinline__ float settle(float x, float m, float s, float c) {
+  float rest;
+  const float d = exact_difference(x, m, rest);
+  const float e = fmaf(-c, s, d), half = 0.5f * s;
+  const bool odd = (int)c & 1;
+  if (e > half || (e == half && (rest > 0.f || (rest == 0.f && odd)))) return c + 1.f;
+  if (e < -half || (e == -half && (rest < 0.f || (rest == 0.f && odd)))) return c - 1.f;
+  return c;
+}
+
+// Smallest and largest of the eight lanes that hold a group, NaN if any is one.
+__device__ __forceinline__ void group_range(float& lo, float& hi) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-    big += x[e] - x[e];  // 0, or NaN where x is a NaN or an infinity
+  for (int off = 1; off < 8; off <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
+}
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Eight channels as loaded, as float32, and the range of their group.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int off = 1; off < kLanes; off <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
-  const unsigned group = kLanes == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
-  const bool odd = (__ballot_sync(0xffffffffu, big != 0.f) & group) != 0;
-  // round down to bfloat16 on the bit pattern
-  uint32_t mb = __float_as_uint(lo);
+  // (smallest, -largest) as one bf16 pair: one shuffle a step for both
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    const uint32_t mn = min2_nan(min2_nan(r.x, r.y), min2_nan(r.z, r.w)), mx = max2_nan(max2_nan(r.x, r.y), max2_nan(r.z, r.w));
+    uint32_t p = min2_nan(__byte_perm(mn, mx, 0x5410) ^ 0x80000000u, __byte_perm(mn, mx, 0x7632) ^ 0x80000000u);
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) p = min2_nan(p, __shfl_xor_sync(0xffffffffu, p, off));
+    lo = __uint_as_float(p << 16);
+    hi = __uint_as_float((p & 0xffff0000u) ^ 0x80000000u);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    lo = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
+    hi = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+    group_range(lo, hi);
+  }
+};
+
+// Codes of eight channels as nibbles (channel e at bits 4e), from the range of
+// their group; sm becomes the packed (s, m).  y = (x - m) * (1/s) in float32 is
+// off by less than 2^-17 (a quotient of at most 15, five half steps of relative
+// 2^-24); only where that could change the nearest integer is the code settled
+// exactly.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, float hi, uint32_t& sm) {
+  uint32_t mb = __float_as_uint(lo);  // rounded down to bfloat16 on the bit pattern
   if ((mb & 0xffffu) && (mb >> 31)) mb += 0x10000u;
   mb &= 0xffff0000u;
   const float m = __uint_as_float(mb);
-  const bool bad = odd || !(fabsf(m) < INFINITY);
+  const bool bad = !(fabsf(hi) < INFINITY && fabsf(m) < INFINITY);
   const float s = round_scale(hi, m);
-  const float r = s > 0.f ? 1.f / s : 0.f;
-  bool near = s > 0.f && !(s >= 0x1p-100f && s <= 0x1p100f);
+  sm = bad ? 0x7fc07fc0u : (__float_as_uint(s) >> 16) | mb;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  if (!(s > 0.f)) r = 0.f;
+  const float2 r2 = make_float2(r, r), nm2 = make_float2(-m, -m), magic = make_float2(12582912.f, 12582912.f);
+  const float2 unmagic = make_float2(-12582912.f, -12582912.f);
+  float far = 0.f;  // distance from the nearest integer
+  float c[8], y[8];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float y = (x[e] - m) * r;
-    const float t = y + 12582912.f;  // 1.5 x 2^23: the nearest integer in the low bits, ties to even
-    c[e] = __float_as_uint(t) & 15u;
-    near |= fabsf(fabsf(y - (t - 12582912.f)) - 0.5f) < 0x1p-18f;
+  for (int i = 0; i < 4; ++i) {
+    const float2 d = tc::fadd2(make_float2(x[2 * i], x[2 * i + 1]), nm2);
+    const float2 t = tc::ffma2(d, r2, magic);  // 1.5 x 2^23 + the nearest integer
+    const float2 f = tc::fadd2(t, unmagic);
+    const float2 e = tc::ffma2(d, r2, make_float2(-f.x, -f.y));
+    c[2 * i] = f.x;
+    c[2 * i + 1] = f.y;
+    y[2 * i] = e.x;
+    y[2 * i + 1] = e.y;
+    far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
   }
-  if (near && !bad) {
+  const bool small = s > 0.f && !(s >= 0x1p-100f && s <= 0x1p100f);
+  if ((far > 0.5f - 0x1p-17f || small) && !bad) {
+    if (small) {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        float v = x[0];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      c[e] = (uint32_t)min(15, max(0, (int)rint(((double)x[e] - (double)m) / (double)s)));
+        for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
+        v = (float)min(15, max(0, (int)rint(((double)v - (double)m) / (double)s)));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = e == k ? v : c[k];
+      }
+    } else {
+      uint32_t todo = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) todo |= fabsf(y[k]) > 0.5f - 0x1p-17f ? 1u << k : 0u;
+      while (todo) {  // rarely more than one
+        const int e = __ffs(todo) - 1;
+        todo &= todo - 1;
+        float v = x[0], n = c[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+          v = e == k ? x[k] : v;
+          n = e == k ? c[k] : n;
+        }
+        n = settle(v, m, s, n);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = e == k ? n : c[k];
+      }
+    }
   }
-  return bad ? 0x7fc07fc0u : (__float_as_uint(s) >> 16) | mb;
+  // four codes as one float32 integer below 2^16, exactly
+  float2 w = make_float2(c[3], c[7]);
+#pragma unroll
+  for (int e = 2; e >= 0; --e) w = tc::ffma2(w, make_float2(16.f, 16.f), make_float2(c[e], c[e + 4]));
+  w = tc::fadd2(w, make_float2(8388608.f, 8388608.f));
+  return __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
 }
 
-template <int E>
-__device__ __forceinline__ void load_channels(const __nv_bfloat16* src, float (&x)[E]) {
-  if (E == 4) {
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(src));
-    x[0] = __uint_as_float(r.x << 16), x[1] = __uint_as_float(r.x & 0xffff0000u);
-    x[E - 2] = __uint_as_float(r.y << 16), x[E - 1] = __uint_as_float(r.y & 0xffff0000u);
-  } else {
-    const uint32_t r = __ldg(reinterpret_cast<const uint32_t*>(src));
-    x[0] = __uint_as_float(r << 16), x[1] = __uint_as_float(r & 0xffff0000u);
+// 8 x 8 nibbles transposed: nibble e of row n -> nibble n of row e
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&a)[8]) {
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t x = a[n], y = a[n + 4];
+    a[n] = __byte_perm(x, y, 0x5410);
+    a[n + 4] = __byte_perm(x, y, 0x7632);
   }
-}
-template <int E>
-__device__ __forceinline__ void load_channels(const float* src, float (&x)[E]) {
-  if (E == 4) {
-    const float4 r = __ldg(reinterpret_cast<const float4*>(src));
-    x[0] = r.x, x[1] = r.y, x[E - 2] = r.z, x[E - 1] = r.w;
-  } else {
-    const float2 r = __ldg(reinterpret_cast<const float2*>(src));
-    x[0] = r.x, x[1] = r.y;
+#pragma unroll
+  for (int h = 0; h < 8; h += 4)
+#pragma unroll
+    for (int n = h; n < h + 2; ++n) {
+      const uint32_t x = a[n], y = a[n + 2];
+      a[n] = __byte_perm(x, y, 0x6240);
+      a[n + 2] = __byte_perm(x, y, 0x7351);
+    }
+#pragma unroll
+  for (int n = 0; n < 8; n += 2) {
+    const uint32_t x = a[n], y = a[n + 1];
+    a[n] = (x & 0x0f0f0f0fu) | (y & 0x0f0f0f0fu) << 4;
+    a[n + 1] = (x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
   }
 }
 
-// Append.  A warp quantises one token's key or value at a time (coalesced
-// loads, four rows in flight); the codes meet in shared memory as bytes, are
-// packed there into the block's final image and leave as 16-byte stores.
+// Append.  A lane quantises eight channels of a token's key or value, D/8 lanes
+// a token, with the next two tokens' loads in flight.  Eight channels of a key are one
+// word of the block; values go through shared memory as nibbles, where a thread
+// transposes eight tokens x eight channels into V's words.  The block's image
+// leaves as 16-byte stores.
+constexpr int kAppendThreads = 128;
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q4_append_kernel(Q4IoArgs a) {
+__global__ void __launch_bounds__(kAppendThreads) q4_append_kernel(Q4IoArgs a) {
   using B = Q4Block<D>;
-  constexpr int E = D / 32, kLanes = kQ4Group / E;
-  constexpr int kPitch = D + 4;  // code row in bytes, padded by a bank
-  __shared__ __align__(16) uint8_t codes[2 * kQ4Tokens * kPitch];
+  constexpr int kRowLanes = D / 8;                       // lanes of a token
+  constexpr int kRowsAtOnce = kAppendThreads / kRowLanes;  // tokens per pass of the block
+  constexpr int kPasses = 2 * kQ4Tokens / kRowsAtOnce;
+  constexpr int kBatch = 2;
+  static_assert(kPasses / 2 % kBatch == 0, "a batch is all keys or all values");
   __shared__ __align__(16) uint8_t image[B::kBytes];
+  __shared__ uint32_t vn[kQ4Tokens][kRowLanes + 1];      // nibbles of the values
   pdl_wait();
   pdl_trigger();
   const int sg = blockIdx.x / a.n_blk, s = sg / a.Hkv, g = sg % a.Hkv;
@@ -125,78 +255,75 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(Q4IoArgs a) {
   const int b = sp.p0 / kQ4Tokens + blockIdx.x % a.n_blk;
   if ((long long)b * kQ4Tokens >= sp.p1 || sp.p0 >= sp.p1) return;
   const int t_lo = max(sp.p0 - b * kQ4Tokens, 0), t_hi = min(sp.p1 - b * kQ4Tokens, kQ4Tokens);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // rows 0..31 keys, 32..63 values; a warp takes rows warp, warp + 8, ...
-  constexpr int kAtOnce = 4;
-  for (int r0 = warp; r0 < 2 * kQ4Tokens; r0 += kAtOnce * (kThreads / 32)) {
-    float x[kAtOnce][E];
+  const int c8 = threadIdx.x % kRowLanes, r_of = threadIdx.x / kRowLanes;
+  // rows 0..31 keys, 32..63 values; this thread's token of pass p is
+  // (p % (kPasses / 2)) * kRowsAtOnce + r_of
+  const long long first = (((long long)s * a.n + (long long)b * kQ4Tokens - sp.start + r_of) * a.Hkv + g) * D + c8 * 8;
+  const T* k_row = static_cast<const T*>(a.k) + first;
+  const T* v_row = static_cast<const T*>(a.v) + first;
+  const long long pass_stride = (long long)kRowsAtOnce * a.Hkv * D;
+  uint32_t* k_word = reinterpret_cast<uint32_t*>(image + r_of * B::kRow + ((c8 % 8) / 2) * (D / 8) + ((c8 / 8) * 2 + c8 % 2) * 4);
+  Raw8<T> next[kBatch];
+  auto fetch = [&](int p0) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int r = r0 + i * (kThreads / 32), kv = r >> 5, t = r & 31;
-      if (t >= t_lo && t < t_hi) {
-        const long long tok = (long long)b * kQ4Tokens + t - sp.start;
-        load_channels(static_cast<const T*>(kv ? a.v : a.k) + (((long long)s * a.n + tok) * a.Hkv + g) * D + lane * E, x[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = 0.f;
-      }
+    for (int i = 0; i < kBatch; ++i) {
+      const int p = (p0 + i) % (kPasses / 2), t = p * kRowsAtOnce + r_of;
+      if (t >= t_lo && t < t_hi) next[i].load((p0 >= kPasses / 2 ? v_row : k_row) + p * pass_stride);
+      else next[i].zero();
     }
+  };
+  fetch(0);
+#pragma unroll 1
+  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+    const bool is_v = p0 >= kPasses / 2;
+    float x[kBatch][8], lo[kBatch], hi[kBatch];
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int r = r0 + i * (kThreads / 32), kv = r >> 5, t = r & 31;
-      uint32_t c[E];
-      const uint32_t sm = quantise<E, kLanes>(x[i], c);
-      if (E == 4) *reinterpret_cast<uint32_t*>(codes + r * kPitch + lane * 4) = c[0] | c[1] << 8 | c[E - 2] << 16 | c[E - 1] << 24;
-      else *reinterpret_cast<uint16_t*>(codes + r * kPitch + lane * 2) = (uint16_t)(c[0] | c[1] << 8);
-      if (lane % kLanes == 0)
-        reinterpret_cast<uint32_t*>(image + (kv ? B::kVs : B::kKs))[t * B::kGroups + lane / kLanes] = sm;
+    for (int i = 0; i < kBatch; ++i) {
+      next[i].get(x[i]);
+      next[i].range(lo[i], hi[i]);
+    }
+    if (p0 + kBatch < kPasses) fetch(p0 + kBatch);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int t0 = (p0 + i) % (kPasses / 2) * kRowsAtOnce;
+      uint32_t sm;
+      const uint32_t w = quantise8(x[i], lo[i], hi[i], sm);
+      if (is_v) vn[t0 + r_of][c8] = w;
+      else k_word[t0 * (B::kRow / 4)] = q4_rotate(w);
+      if (c8 % 8 == 0)
+        reinterpret_cast<uint32_t*>(image + (is_v ? B::kVs : B::kKs))[(t0 + r_of) * B::kGroups + c8 / 8] = sm;
     }
   }
   __syncthreads();
-  // K words: eight channels of a token
-  for (int w = threadIdx.x; w < kQ4Tokens * (D / 8); w += kThreads) {
-    const int t = w / (D / 8), c8 = w % (D / 8);
-    const uint32_t* c = reinterpret_cast<const uint32_t*>(codes + t * kPitch + c8 * 8);
-    const uint32_t x = c[0], y = c[1];
-    *reinterpret_cast<uint32_t*>(image + t * B::kRow + ((c8 % 8) / 2) * (D / 8) + ((c8 / 8) * 2 + c8 % 2) * 4) =
-        q4_pack((x & 0xffu) | (x & 0xff00u) << 8, (x >> 16 & 0xffu) | (x >> 24) << 16, (y & 0xffu) | (y & 0xff00u) << 8,
-                (y >> 16 & 0xffu) | (y >> 24) << 16);
-  }
-  // V words: eight tokens of a channel; a thread takes four channels
-  for (int w = threadIdx.x; w < D; w += kThreads) {
-    const int d4 = w % (D / 4), tig = w / (D / 4);
-    uint32_t x[8];
+  if (threadIdx.x < kRowLanes * 4) {
+    const int j = threadIdx.x % kRowLanes, tig = threadIdx.x / kRowLanes;
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = (i >> 2) * 16 + ((i >> 1) & 1) * 8 + 2 * tig + (i & 1);
-      x[i] = *reinterpret_cast<const uint32_t*>(codes + (kQ4Tokens + t) * kPitch + d4 * 4);
+    for (int n = 0; n < 8; ++n) {
+      const int f = q4_field_of(n);  // field f: tokens 16 (f/2) + 8 (f%2) + 2 tig and the next
+      w[n] = vn[(f >> 1) * 16 + (f & 1) * 8 + 2 * tig + q4_half_of(n)][j];
     }
+    transpose_nibbles(w);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t p[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f)  // byte e of two tokens into the halves
-        p[f] = (x[2 * f] >> (8 * e) & 0xffu) | (x[2 * f + 1] >> (8 * e) & 0xffu) << 16;
-      *reinterpret_cast<uint32_t*>(image + B::kV + q4_v_word(d4 * 4 + e, tig)) = q4_pack(p[0], p[1], p[2], p[3]);
-    }
+    for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(image + B::kV + q4_v_word(j * 8 + e, tig)) = q4_rotate(w[e]);
   }
   __syncthreads();
   uint8_t* blk = static_cast<uint8_t*>(a.cache) + ((long long)sg * a.cap_blk + b) * B::kBytes;
   if (t_lo == 0 && t_hi == kQ4Tokens) {
-    for (int w = threadIdx.x; w < B::kBytes / 16; w += kThreads)
+    for (int w = threadIdx.x; w < B::kBytes / 16; w += kAppendThreads)
       reinterpret_cast<uint4*>(blk)[w] = reinterpret_cast<const uint4*>(image)[w];
     return;
   }
   // a partly covered block: K rows and scales of its tokens, V words merged
-  for (int w = threadIdx.x; w < B::kV / 4; w += kThreads)
+  for (int w = threadIdx.x; w < B::kV / 4; w += kAppendThreads)
     if (w / (B::kRow / 4) >= t_lo && w / (B::kRow / 4) < t_hi)
       reinterpret_cast<uint32_t*>(blk)[w] = reinterpret_cast<const uint32_t*>(image)[w];
-  for (int w = threadIdx.x; w < 2 * kQ4Tokens * B::kGroups; w += kThreads) {
+  for (int w = threadIdx.x; w < 2 * kQ4Tokens * B::kGroups; w += kAppendThreads) {
     const int t = w / B::kGroups % kQ4Tokens;
     if (t >= t_lo && t < t_hi)
       reinterpret_cast<uint32_t*>(blk + B::kKs)[w] = reinterpret_cast<const uint32_t*>(image + B::kKs)[w];
   }
-  for (int w = threadIdx.x; w < B::kV / 16; w += kThreads) {
+  for (int w = threadIdx.x; w < B::kV / 16; w += kAppendThreads) {
     uint32_t keep[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
@@ -281,8 +408,8 @@ __global__ void __launch_bounds__(D) q4_read_kernel(Q4IoArgs a) {
       float v[8];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        v[2 * f] = low_value(field_of(x, f), sc, m);
-        v[2 * f + 1] = high_value(field_of(x, f), sc, m);
+        v[q4_k_channel(f, 0)] = low_value(field_of(x, f), sc, m);
+        v[q4_k_channel(f, 1)] = high_value(field_of(x, f), sc, m);
       }
       store_channels(static_cast<T*>(a.k_out) + (row0 + (long long)t * a.Hkv) * D + c8 * 8, v);
     }
@@ -296,10 +423,10 @@ cudaError_t launch_q4_append(Q4IoArgs a, int dtype, int d, cudaStream_t st, bool
   a.n_blk = min(a.cap_blk, (a.n + kQ4Tokens - 1) / kQ4Tokens + 1);
   const dim3 grid((unsigned)((long long)a.S * a.Hkv * a.n_blk));
   if (dtype == kDtypeBF16)
-    return d == 128 ? launch_kernel(q4_append_kernel<__nv_bfloat16, 128>, grid, dim3(kThreads), 0, st, pdl, a)
-                    : launch_kernel(q4_append_kernel<__nv_bfloat16, 64>, grid, dim3(kThreads), 0, st, pdl, a);
-  return d == 128 ? launch_kernel(q4_append_kernel<float, 128>, grid, dim3(kThreads), 0, st, pdl, a)
-                  : launch_kernel(q4_append_kernel<float, 64>, grid, dim3(kThreads), 0, st, pdl, a);
+    return d == 128 ? launch_kernel(q4_append_kernel<__nv_bfloat16, 128>, grid, dim3(kAppendThreads), 0, st, pdl, a)
+                    : launch_kernel(q4_append_kernel<__nv_bfloat16, 64>, grid, dim3(kAppendThreads), 0, st, pdl, a);
+  return d == 128 ? launch_kernel(q4_append_kernel<float, 128>, grid, dim3(kAppendThreads), 0, st, pdl, a)
+                  : launch_kernel(q4_append_kernel<float, 64>, grid, dim3(kAppendThreads), 0, st, pdl, a);
 }
 
 cudaError_t launch_q4_read(Q4IoArgs a, int dtype, int d, cudaStream_t st) {

@@ -25,9 +25,14 @@
 //   V: word (channel d, tig) holds the tokens {2 tig, 2 tig + 1, 8 + 2 tig,
 //      9 + 2 tig} and the same + 16; d = 8 j + gid sits in chunk j/4, lane
 //      4 gid + tig, word j%4.
-// Inside a word the eight codes are four pairs (field f: codes 2f in the low
-// half, 2f + 1 in the high half) placed so that one shift or rotation and one
-// and-or turn a pair into two fp16 numbers 16 + c (code at mantissa bits 6..9).
+// Inside a word the eight codes are four pairs (field f: one code in the low
+// half, one in the high), placed so that one shift or rotation and one and-or
+// turn a pair into two fp16 numbers 16 + c (code at mantissa bits 6..9).  As
+// nibbles, rotated left by two bits, a word is
+//   n      0    1    2    3    4    5    6    7
+//   field  2 l  0 l  1 l  3 h  2 h  0 h  1 h  3 l      (l, h: low, high half)
+// K: nibble n is channel n of the word's eight.  V: field f holds the tokens
+// 16 (f/2) + 8 (f%2) + 2 tig (low) and the next (high).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -67,11 +72,19 @@ __device__ __forceinline__ uint32_t q4_field(uint32_t x) {
   if (F == 3) x = __funnelshift_l(x, x, 8);
   return x & kQ4Mask;
 }
-// code i (0..7) of a word
-__device__ __forceinline__ int q4_code(uint32_t x, int i) {
-  const int f = i >> 1;
-  x = f == 0 ? x : f == 1 ? x >> 4 : f == 2 ? x << 4 : __funnelshift_l(x, x, 8);
-  return (int)((x >> (6 + 16 * (i & 1))) & 15u);
+// Field and half of nibble n, and the K channel of (field, half).
+__host__ __device__ __forceinline__ constexpr int q4_field_of(int n) { return 0x31023102 >> (4 * n) & 3; }
+__host__ __device__ __forceinline__ constexpr int q4_half_of(int n) { return 0x78 >> n & 1; }
+__host__ __device__ __forceinline__ constexpr int q4_k_channel(int f, int half) {
+  return (half ? 0x3465 : 0x7021) >> (4 * f) & 7;
+}
+// Eight nibbles -> word, and nibble n of a word.
+__device__ __forceinline__ uint32_t q4_rotate(uint32_t nibbles) { return __funnelshift_l(nibbles, nibbles, 2); }
+__device__ __forceinline__ int q4_nibble(uint32_t x, int n) { return (int)(__funnelshift_r(x, x, 2) >> (4 * n) & 15u); }
+// Nibble of the V word that holds block token t.
+__device__ __forceinline__ int q4_v_nibble(int t) {
+  const int f = (t >> 4) * 2 + ((t >> 3) & 1);
+  return (t & 1) ? (0x3465 >> (4 * f) & 7) : (0x7021 >> (4 * f) & 7);
 }
 
 __device__ __forceinline__ float q4_scale(uint32_t sm) { return __uint_as_float(sm << 16); }

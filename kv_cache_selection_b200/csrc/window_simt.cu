@@ -28,8 +28,8 @@ __device__ __forceinline__ void load_block(float (*ks)[D + 1], float (*vs)[D + 1
     const uint32_t sv = reinterpret_cast<const uint32_t*>(blk + B::kVs)[t * B::kGroups + g];
     const uint32_t xk = *reinterpret_cast<const uint32_t*>(blk + t * B::kRow + (r / 16) * (D / 8) + (g * 2 + (r % 16) / 8) * 4);
     const uint32_t xv = *reinterpret_cast<const uint32_t*>(blk + B::kV + q4_v_word(d, (t & 7) >> 1));
-    ks[t][d] = fmaf((float)q4_code(xk, r % 8), q4_scale(sk), q4_min(sk));
-    vs[t][d] = fmaf((float)q4_code(xv, (t >> 4) * 4 + ((t >> 3) & 1) * 2 + (t & 1)), q4_scale(sv), q4_min(sv));
+    ks[t][d] = fmaf((float)q4_nibble(xk, r % 8), q4_scale(sk), q4_min(sk));
+    vs[t][d] = fmaf((float)q4_nibble(xv, q4_v_nibble(t)), q4_scale(sv), q4_min(sv));
   }
 }
 
