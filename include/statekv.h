@@ -373,6 +373,12 @@ int statekv_q4_decode(const void* cache, int n_streams, int Hq, int Hkv, int d, 
  * statekv_status on a bad shape. */
 long long statekv_q4_decode_workspace(int n_streams, int Hq, int Hkv, int d, int n_text, int dtype);
 
+/* Device-side status of the statekv_q4_decode calls on the current device: *code
+ * = 0, or the first error a kernel recorded since the last call (a pipeline
+ * wait that exceeded its time limit, as in statekv_device_status; the results
+ * of that call are invalid).  Synchronises the device, then resets the word. */
+int statekv_q4_status(int* code);
+
 /* Causal self-attention over n_tokens tokens with a sliding window and first
  * tokens that stay visible: token i attends to the tokens j <= i with
  * j > i - window or j < n_sink.  (The windowed counterpart of

@@ -157,12 +157,15 @@ struct WindowArgs {
   float scale_log2;          // log2(e)/sqrt(d)
 };
 
-// Attention over the 4-bit cache in W workers per tile of query rows.
+// Attention over the 4-bit cache in tiles of query rows (text token i, head h of
+// the KV head's G: row i * G + h).  rows = 8 or 16: W workers per tile over all
+// (stream, KV head), partials [tiles][W + S * Hkv]; rows = 128: W splits per
+// (stream, KV head, tile), partials [S][Hkv][tiles][W].
 struct Q4AttnArgs {
   WindowArgs w;
-  float* part_o;             // [row tiles][W + S * Hkv][rows][d] unnormalised O
-  float* part_ml;            // [row tiles][W + S * Hkv][rows][2] log2 maximum, sum
-  int W, rows;               // workers; query rows per tile
+  float* part_o;             // [partials][rows][d] unnormalised O
+  float* part_ml;            // [partials][rows][2] log2 maximum, sum
+  int W, rows, n_rb;
 };
 
 // Cached tokens of stream s, clipped to the cache.

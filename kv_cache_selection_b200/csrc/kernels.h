@@ -121,6 +121,9 @@ struct Q4Plan {
 };
 Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm);
 cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st);
+// Its kernel for 128-row tiles (tensor cores), and the first error its waits recorded.
+cudaError_t launch_q4_attn_tc(const Q4AttnArgs& p, int d, cudaStream_t st);
+cudaError_t q4_attn_tc_status(int* code);
 cudaError_t launch_window_simt(const WindowArgs& a, int dtype, int d, cudaStream_t st);
 // The same without a cache on the tensor cores (bf16, window >= 1), and the first error its waits recorded.
 cudaError_t launch_window_tc(const WindowArgs& a, int d, cudaStream_t st);

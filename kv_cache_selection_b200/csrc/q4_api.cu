@@ -273,6 +273,13 @@ int sink_window_prefill(const void* q, const void* k, const void* v, int n_token
   return sink_window_prefill_batched(q, k, v, 1, n_tokens, Hq, Hkv, d, dtype, window, n_sink, out, lse, stream);
 }
 
+int statekv_q4_status(int* code) {
+  if (!code) return fail(STATEKV_ERR_INVALID_ARG, "null argument");
+  const cudaError_t e = skv::q4_attn_tc_status(code);
+  if (e != cudaSuccess) return fail(STATEKV_ERR_CUDA, "status read failed: %s", cudaGetErrorString(e));
+  return STATEKV_OK;
+}
+
 int sink_window_status(int* code) {
   if (!code) return fail(STATEKV_ERR_INVALID_ARG, "null argument");
   const cudaError_t e = skv::window_tc_status(code);

@@ -31,6 +31,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_cache.cuh"
+#include "q4_visible.cuh"
 #include "tc_common.cuh"
 
 namespace skv {
@@ -75,27 +76,6 @@ template <int F>
 __device__ __forceinline__ uint32_t code_centred(uint32_t x) {
   const uint32_t r = code_raw<F>(x);
   return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&r), __half2half2(__ushort_as_half(0x4E00))));  // 24
-}
-
-// Blocks of a stream that any row sees: [0, sinks) and [window, n).
-struct Visible {
-  int L, sinks, window, n;
-  __device__ __forceinline__ int count() const { return sinks + n - window; }
-  __device__ __forceinline__ int block(int v) const { return v < sinks ? v : v - sinks + window; }
-};
-__device__ __forceinline__ Visible visible_of(const WindowArgs& a, int s) {
-  Visible x;
-  x.L = q4_length(a, s);
-  x.n = (x.L + kQ4Tokens - 1) / kQ4Tokens;
-  x.sinks = 0;
-  x.window = 0;
-  if (a.window) {
-    x.sinks = (min(a.n_sink, x.L) + kQ4Tokens - 1) / kQ4Tokens;
-    const long long lo = (long long)x.L - a.window + 1;  // first token of row 0's window
-    x.window = lo >= x.L ? x.n : lo > 0 ? (int)(lo / kQ4Tokens) : 0;
-    x.window = max(x.window, x.sinks);
-  }
-  return x;
 }
 
 // The numbering of the visible blocks: of (s, g), first block and count; and
@@ -573,8 +553,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
     join(t, 1.f, v);
   }
   pdl_wait();
-  const Deal deal = deal_of(a, p.W);
-  if (vis.count() > 0) {
+  int w0 = 0, w1 = -1, r = 0;
+  long long part0 = 0;
+  const int sg = s * a.Hkv + g;
+  if (p.rows == 128) {  // the tensor-core kernel: W partials per (stream, KV head, row tile)
+    part0 = ((long long)sg * p.n_rb + row / 128) * p.W;
+    r = row % 128;
+    w1 = p.W - 1;
+  } else if (vis.count() > 0) {
+    const Deal deal = deal_of(a, p.W);
     long long base = 0;
     if (a.lengths) {
       for (int s2 = 0; s2 < s; ++s2) base += visible_of(a, s2).count();
@@ -582,10 +569,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
       base = (long long)s * vis.count();
     }
     base = base * a.Hkv + (long long)g * vis.count();
-    const int w0 = deal.owner(base), w1 = deal.owner(base + vis.count() - 1);
-    const int sg = s * a.Hkv + g;
-    const long long part0 = (long long)(row / p.rows) * (p.W + a.S * a.Hkv) + sg;
-    const int r = row % p.rows;
+    w0 = deal.owner(base);
+    w1 = deal.owner(base + vis.count() - 1);
+    part0 = (long long)(row / p.rows) * (p.W + a.S * a.Hkv) + sg;
+    r = row % p.rows;
+  }
+  {
     constexpr int kBatch = 4;
     for (int w = w0 + warp; w <= w1; w += kMergeWarps * kBatch) {
       float2 ml[kBatch];
@@ -630,18 +619,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
   }
 }
 
+template <typename T, int D>
+cudaError_t launch_merge(const Q4AttnArgs& p, cudaStream_t st) {
+  const long long rows = (long long)p.w.S * p.w.Hq * p.w.n;
+  return launch_kernel(q4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(kMergeWarps * 32), 0, st, true, p);
+}
+
 template <typename T, int D, int NT, int NS>
-cudaError_t launch(const Q4AttnArgs& p, int n_rb, cudaStream_t st) {
+cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
   using B = Q4Block<D>;
   constexpr int ring = kWarps * kStages * B::kBytes;
   constexpr int merge = kWarps * 8 * NT * (D + 4 + 2) * 4;
   constexpr int smem = ring > merge ? ring : merge;
   cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS>, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(q4_attn_kernel<T, D, NT, NS>, dim3(p.W, n_rb), dim3(kWarps * 32), smem, st, false, p);
-  if (e != cudaSuccess) return e;
-  const long long rows = (long long)p.w.S * p.w.Hq * p.w.n;
-  return launch_kernel(q4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(kMergeWarps * 32), 0, st, true, p);
+  e = launch_kernel(q4_attn_kernel<T, D, NT, NS>, dim3(p.W, p.n_rb), dim3(kWarps * 32), smem, st, false, p);
+  return e != cudaSuccess ? e : launch_merge<T, D>(p, st);
 }
 
 }  // namespace
@@ -649,10 +642,17 @@ cudaError_t launch(const Q4AttnArgs& p, int n_rb, cudaStream_t st) {
 Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm) {
   Q4Plan pl{};
   const long long R = (long long)(Hq / Hkv) * n;
-  pl.rows = dtype == kDtypeF32 || R <= 8 ? 8 : 16;
+  pl.rows = dtype == kDtypeF32 || R <= 8 ? 8 : R <= 16 ? 16 : 128;
   pl.n_rb = (int)((R + pl.rows - 1) / pl.rows);
-  pl.W = std::max(1, n_sm / pl.n_rb);
-  const size_t parts = (size_t)pl.n_rb * (pl.W + (size_t)S * Hkv) * pl.rows;
+  const long long sg = (long long)S * Hkv;
+  size_t parts;
+  if (pl.rows == 128) {
+    pl.W = (int)std::max(1ll, n_sm / (sg * pl.n_rb));
+    parts = (size_t)sg * pl.n_rb * pl.W * 128;
+  } else {
+    pl.W = std::max(1, n_sm / pl.n_rb);
+    parts = (size_t)pl.n_rb * (pl.W + sg) * pl.rows;
+  }
   pl.o_bytes = parts * d * 4;
   pl.bytes = pl.o_bytes + parts * 8;
   return pl;
@@ -663,14 +663,20 @@ cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspac
   p.w = a;
   p.W = pl.W;
   p.rows = pl.rows;
+  p.n_rb = pl.n_rb;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.o_bytes);
-  if (dtype == kDtypeF32) {
-    return d == 128 ? launch<float, 128, 1, 2>(p, pl.n_rb, st) : launch<float, 64, 1, 2>(p, pl.n_rb, st);
-  }
-  if (pl.rows == 8)
-    return d == 128 ? launch<__nv_bfloat16, 128, 1, 1>(p, pl.n_rb, st) : launch<__nv_bfloat16, 64, 1, 1>(p, pl.n_rb, st);
-  return d == 128 ? launch<__nv_bfloat16, 128, 2, 1>(p, pl.n_rb, st) : launch<__nv_bfloat16, 64, 2, 1>(p, pl.n_rb, st);
+  if (dtype == kDtypeF32) return d == 128 ? launch<float, 128, 1, 2>(p, st) : launch<float, 64, 1, 2>(p, st);
+  if (pl.rows == 8) return d == 128 ? launch<__nv_bfloat16, 128, 1, 1>(p, st) : launch<__nv_bfloat16, 64, 1, 1>(p, st);
+  if (pl.rows == 16) return d == 128 ? launch<__nv_bfloat16, 128, 2, 1>(p, st) : launch<__nv_bfloat16, 64, 2, 1>(p, st);
+  // no more splits than 128-token tiles can be visible
+  const long long len = a.lengths ? a.capacity : a.length;
+  long long blocks = (len + 31) / 32;
+  if (a.window) blocks = std::min(blocks, (std::min<long long>(a.n_sink, len) + 31) / 32 + (a.window + 31ll) / 32 + 1);
+  p.W = (int)std::max(1ll, std::min((long long)p.W, (blocks + 3) / 4));
+  const cudaError_t e = launch_q4_attn_tc(p, d, st);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? launch_merge<__nv_bfloat16, 128>(p, st) : launch_merge<__nv_bfloat16, 64>(p, st);
 }
 
 }  // namespace skv

@@ -65,6 +65,7 @@ _SIGS = {
                                ctypes.c_longlong, _vp]),
     "statekv_q4_decode_workspace": (ctypes.c_longlong, [_i, _i, _i, _i, _i, _i]),
     "sink_window_prefill": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "statekv_q4_status": (_i, [_ip]),
     "sink_window_status": (_i, [_ip]),
     "sink_window_prefill_batched": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
 }
@@ -464,6 +465,14 @@ class Q4Cache:
                                          out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
                                          need, _stream_ptr(stream, self._dev)))
         return out, lse
+
+
+def q4_status() -> int:
+    """0, or the first error code that Q4Cache.decode's kernels recorded on the
+    current device since the last call (synchronises)."""
+    code = ctypes.c_int()
+    _check(lib.statekv_q4_status(ctypes.byref(code)))
+    return code.value
 
 
 def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=True, stream=None):

@@ -238,6 +238,7 @@ def test_decode_matches_oracle(S, Hq, Hkv, d, length, n, window, n_sink, dtype):
         check_attention(out[s], lse[s], wants[s], dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
     again, _ = c.decode(ins[0].cuda(), ins[1].cuda(), ins[2].cuda(), ins[3], window=window, n_sink=n_sink)
     assert same(out, again)        # no order of arrival in any sum
+    assert _skv().q4_status() == 0
 
 
 @cuda
