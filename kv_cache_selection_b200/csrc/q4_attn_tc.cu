@@ -7,13 +7,14 @@
 // 128-token key tiles.  Per key tile
 //   raw blocks -> shared memory          one warp, bulk copies into a ring
 //   K, V -> fp16 in shared memory        a warpgroup each
-//   S = Q K^T, O += P V                  tcgen05, fp16 in, float32 accumulate
-//   P = 2^(S c - m)                      softmax warpgroup, thread = row
-// with S double-buffered in tensor memory.
+//   S = Q K^T, O += P V                  one thread; tcgen05, fp16 in, float32 accumulate
+//   P = 2^(S c - m)                      two warpgroups, thread = 64 columns of a row
+// with S double-buffered in tensor memory.  The two halves of a row share its
+// lazy maximum: one barrier a tile tells whether either wants to raise it.
 //
-// With numbers scaled by a power of two per tile (its largest magnitude into
-// [1, 2)) fp16 serves the cache's whole range; the tile's exponent returns in
-// S's scale (K) and in P's (V, relative to the largest V tile so far).
+// Keys and values are scaled by powers of two that bring the largest magnitude in
+// the block's range of tokens (read off the scales beforehand) into [2^12, 2^13),
+// so fp16 serves the cache's range: full precision down to 2^-26 of the largest.
 //   K: (c - 8) s has 11 bits and is exact in fp16; the groups' m + 8 s times the
 //     sums of q enter as one more product of depth 16, both sides in two fp16
 //     parts.  So S is as exact as its float32 sums.
@@ -25,6 +26,8 @@
 // their 32-token block, so K's rows (S's columns) take the same order; a K word
 // is a chunk of its row with the channels in field order, Q alike.  No value
 // moves between threads.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_cache.cuh"
@@ -35,15 +38,10 @@ namespace skv {
 namespace {
 using namespace tc;
 
-constexpr int kThreads = 512;
-// registers: launched at 128 a thread; loader and MMA issuer 64, softmax 208,
-// the two dequantising warpgroups 112: 64 + 208 + 2 x 112 <= 4 x 128
-constexpr int kRegsLow = 64, kRegsSoftmax = 208, kRegsDequant = 112;
-static_assert(kRegsLow + kRegsSoftmax + 2 * kRegsDequant <= 4 * 128, "register split exceeds the launch");
+constexpr int kThreads = 640;
 constexpr int kRaw = 3;          // raw tiles in flight
 constexpr float kRaise = 8.0f;   // log2 headroom of the lazy row maximum
 constexpr int kPShift = 6;       // P is held as P 2^6 (below 2^14)
-constexpr int kTileTokens = 128;
 
 __device__ int g_err;  // first error of the pipeline waits of all calls on a device
 
@@ -60,14 +58,18 @@ struct Smem {
   static constexpr int kRawTile = 4 * B::kBytes;
   static constexpr int kKx = kV + 2 * 2 * kVAtom;       // two tiles of 128 rows x 16 fp16, no swizzle
   static constexpr int kRawAt = kKx + 2 * 4096;
-  static constexpr int kQs = kRawAt + kRaw * kRawTile;   // group sums of q [128][groups]
-  static constexpr int kTab = kQs + 128 * B::kGroups * 4;  // V scales: [4 blk][4 tig][groups][4 f] (s pair, mid pair)
-  static constexpr int kRow = kTab + 16 * B::kGroups * 32;  // row scales [128]
-  static constexpr int kExp = kRow + 512;                // exponents K[4], V[4]; maxima [2][2][4]
-  static constexpr int kPoison = kExp + 32 + 64;         // [4 tiles][groups][4 words]
+  static constexpr int kTabBytes = 16 * B::kGroups * 32;  // V scales: [4 blk][4 tig][groups][4 f] (s pair, mid pair)
+  static constexpr int kTab = kRawAt + kRaw * kRawTile;
+  static constexpr int kHalfMax = kTab + kTabBytes;  // [2][128] float32
+  static constexpr int kTop = kHalfMax + 1024;           // largest magnitudes of K, V (float32 bits)
+  static constexpr int kPoison = kTop + 16;              // [4 tiles][groups][4 words]
   static constexpr int kBar = kPoison + 4 * B::kGroups * 16;
-  // raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], q, pv, o, done, qx
-  static constexpr int kNumBars = 2 * kRaw + 12 + 5;
+  // read before the second K tile is written: row scales [128], group sums of q [128][groups]
+  static constexpr int kRow = kK + kTile;
+  static constexpr int kQs = kRow + 512;
+  // raw_full[kRaw], raw_empty[kRaw], k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], qx, pv, o,
+  // done
+  static constexpr int kNumBars = 2 * kRaw + 12 + 4;
   static constexpr int kTmem = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmem + 4;
   static constexpr int kBytes = kAbort + 4;
@@ -114,13 +116,28 @@ __device__ __forceinline__ uint32_t dequant(uint32_t w, uint32_t s, uint32_t mid
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
 
+// Token `at` of the visible block number v: seen by some row of the tile, by
+// every row of the tile.
+struct Token {
+  bool some, every;
+};
+__device__ __forceinline__ Token token_of(const WindowArgs& a, const Visible& vis, int v, int at, int i_first, int i_last) {
+  const int tok = v < vis.count() ? vis.block(v) * kQ4Tokens + at : 0x7fffffff;
+  const bool keep = !a.window || tok < a.n_sink;
+  Token t;
+  t.some = tok < vis.L && (keep || (long long)tok > (long long)vis.L + i_first - a.window);
+  t.every = keep || (long long)tok > (long long)vis.L + i_last - a.window;
+  return t;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   using L = Smem<D>;
   using B = Q4Block<D>;
   constexpr int NG = B::kGroups;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: the compiler has to see shared memory)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t sb = smem_u32(smem);
   const WindowArgs& a = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -147,13 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   auto v_empty = [&](int i) { return bar(2 * kRaw + 6 + i); };
   auto s_full = [&](int i) { return bar(2 * kRaw + 8 + i); };
   auto p_full = [&](int i) { return bar(2 * kRaw + 10 + i); };
-  const uint32_t q_full = bar(2 * kRaw + 12), pv_done = bar(2 * kRaw + 13), o_done = bar(2 * kRaw + 14), all_done = bar(2 * kRaw + 15),
-                 qx_full = bar(2 * kRaw + 16);
+  const uint32_t qx_full = bar(2 * kRaw + 12), pv_done = bar(2 * kRaw + 13), o_done = bar(2 * kRaw + 14),
+                 all_done = bar(2 * kRaw + 15);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmem);
-  int* exp_k = reinterpret_cast<int*>(smem + L::kExp);
-  int* exp_v = exp_k + 4;
-  float* maxima = reinterpret_cast<float*>(exp_k + 8);  // [K, V][2][4 warps]
+  uint32_t* tops = reinterpret_cast<uint32_t*>(smem + L::kTop);
+  float* half_max = reinterpret_cast<float*>(smem + L::kHalfMax);
   uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPoison);
   int* err = &g_err;
 
@@ -168,14 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       mbar_init(v_full(i), 4);
       mbar_init(v_empty(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
+      mbar_init(p_full(i), 8);
     }
-    mbar_init(q_full, 4);
-    mbar_init(qx_full, 4);
+    mbar_init(qx_full, 8);
     mbar_init(pv_done, 1);
     mbar_init(o_done, 1);
     mbar_init(all_done, 1);
     *abort_flag = 0;
+    tops[0] = tops[1] = 0u;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -187,24 +203,100 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
+  const uint8_t* base = static_cast<const uint8_t*>(a.cache) + (long long)sg * a.cap_blk * B::kBytes;
+  auto load_raw = [&](int j) {
+    const int v0 = (t_begin + j) * 4, nb = min(4, vis.count() - v0), sl = j % kRaw;
+    mbar_arrive_expect_tx(raw_full(sl), nb * B::kBytes);
+    for (int b = 0; b < nb; ++b)
+      bulk_load(sb + L::kRawAt + sl * L::kRawTile + b * B::kBytes, base + (long long)vis.block(v0 + b) * B::kBytes,
+                B::kBytes, raw_full(sl));
+  };
+  if (threadIdx.x == 0)
+    for (int j = 0; j < min(n, kRaw); ++j) load_raw(j);
+  // the largest |m + 8 s| + 8 s of the visible tokens' groups, K and V: an upper
+  // bound of every value (a maximum, so the order of the atomics does not matter)
+  if (warp > 0 && (warp < 12 || warp >= 16)) {
+    float top[2] = {0.f, 0.f};
+    const int end = min((t_begin + n) * 4, vis.count()) * kQ4Tokens;
+    const int mine = warp < 12 ? threadIdx.x - 32 : threadIdx.x - 160;  // 480 threads
+    using Words = typename std::conditional<NG == 2, uint2, uint32_t>::type;
+#pragma unroll 4
+    for (int x = t_begin * 4 * kQ4Tokens + mine; x < end; x += 480) {
+      const Token t = token_of(a, vis, x / kQ4Tokens, x % kQ4Tokens, i_first, i_last);
+      const uint8_t* blk = base + (long long)vis.block(x / kQ4Tokens) * B::kBytes + (x % kQ4Tokens) * (NG * 4);
+      const Words kw = __ldg(reinterpret_cast<const Words*>(blk + B::kKs)), vw = __ldg(reinterpret_cast<const Words*>(blk + B::kVs));
+#pragma unroll
+      for (int w = 0; w < 2 * NG; ++w) {
+        const uint32_t sm = reinterpret_cast<const uint32_t*>(w < NG ? &kw : &vw)[w % NG];
+        const float sc = q4_scale(sm), y = fmaf(sc, 8.f, fabsf(fmaf(sc, 8.f, q4_min(sm))));
+        if (t.some) top[w / NG] = fmaxf(top[w / NG], y);
+      }
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+      for (int off = 16; off; off >>= 1) top[kv] = fmaxf(top[kv], __shfl_xor_sync(0xffffffffu, top[kv], off));
+      if (lane == 0) atomicMax(tops + kv, __float_as_uint(top[kv]));
+    }
+  }
+  if (warp >= 12 && warp < 16) {
+    // Q: thread = row, scaled by a power of two, channels of a chunk in field order
+    const int tid = threadIdx.x - 384, row = row0 + tid, rr = min(row, R - 1);
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                    (((long long)s * a.n + rr / G) * a.Hq + g * G + rr % G) * D);
+    uint4 x[D / 8];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) x[c] = __ldg(q + c);
+    float top = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&x[c])[e];
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+      }
+    int ex = (int)(__float_as_uint(top) >> 23);
+    ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, 12);
+    const float up = row < R ? __uint_as_float((uint32_t)(264 - ex) << 23) : 0.f;
+    reinterpret_cast<float*>(smem + L::kRow)[tid] = __uint_as_float((uint32_t)(ex - 10) << 23) * a.scale_log2;
+    float sum[NG];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      float y[8], t = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&x[c])[e];
+        y[2 * e] = __uint_as_float(w << 16) * up;
+        y[2 * e + 1] = __uint_as_float(w & 0xffff0000u) * up;
+        t += y[2 * e] + y[2 * e + 1];
+      }
+      sum[c >> 3] = (c & 7) ? sum[c >> 3] + t : t;
+      uint4 o;
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        reinterpret_cast<uint32_t*>(&o)[f] = pack_half2(y[q4_k_channel(f, 0)], y[q4_k_channel(f, 1)]);
+      *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kAtom + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = o;
+    }
+#pragma unroll
+    for (int gg = 0; gg < NG; ++gg) reinterpret_cast<float*>(smem + L::kQs)[tid * NG + gg] = sum[gg];
+    for (int b = 0; b < 2; ++b)  // the unused half of the depth-16 rows
+      *reinterpret_cast<uint4*>(smem + L::kKx + b * 4096 + 2048 + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async();
+  }
+  __syncthreads();
+  // exponents that bring it into [2^12, 2^13)
+  const int eK = min(max((int)(tops[0] >> 23) - 127 - 12, -100), 100), eV = min(max((int)(tops[1] >> 23) - 127 - 12, -100), 100);
   auto col_s = [](int x) { return (uint32_t)(x * 128); };
   constexpr uint32_t kColO = 256, kColQx = 384;
 
   if (warp < 4) {
-    regs_dec<kRegsLow>();
     if (warp == 0) {
       // ---------------------------------------------------------- loader
       if (lane == 0) {
-        const uint8_t* base = static_cast<const uint8_t*>(a.cache) + (long long)sg * a.cap_blk * B::kBytes;
-        int issued = 0;
-        for (int j = 0; j < n; ++j) {
-          const int sl = j % kRaw;
-          if (!mbar_wait(raw_empty(sl), ((j / kRaw) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
-          const int v0 = (t_begin + j) * 4, nb = min(4, vis.count() - v0);
-          mbar_arrive_expect_tx(raw_full(sl), nb * B::kBytes);
-          for (int b = 0; b < nb; ++b)
-            bulk_load(sb + L::kRawAt + sl * L::kRawTile + b * B::kBytes, base + (long long)vis.block(v0 + b) * B::kBytes,
-                      B::kBytes, raw_full(sl));
+        int issued = min(n, kRaw);
+        for (int j = issued; j < n; ++j) {
+          if (!mbar_wait(raw_empty(j % kRaw), ((j / kRaw) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
+          load_raw(j);
           issued = j + 1;
         }
         for (int j = max(0, issued - kRaw); j < issued; ++j) drain_wait(raw_full(j % kRaw), (j / kRaw) & 1, err);
@@ -227,8 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
           mma_commit(s_full(j & 1));
           mma_commit(k_empty(j & 1));
         };
-        bool ok = mbar_wait(q_full, 0, err, kErrWaitLoad, abort_flag) &&
-                  mbar_wait(qx_full, 0, err, kErrWaitLoad, abort_flag) &&
+        bool ok = mbar_wait(qx_full, 0, err, kErrWaitLoad, abort_flag) &&
                   mbar_wait(k_full(0), 0, err, kErrWaitLoad, abort_flag);
         if (ok) {
           fence_after_sync();
@@ -246,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
           const uint64_t v0 = dv + (uint64_t)((j & 1) * (2 * L::kVAtom >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + kColO, tmem + col_s(j & 1) + kk * 8, v0 + (uint64_t)(((kk >> 2) * L::kVAtom + (kk & 3) * 32) >> 4),
+            mma_ts(tmem + kColO, tmem + col_s(j & 1) + (kk >> 2) * 64 + (kk & 3) * 8, v0 + (uint64_t)(((kk >> 2) * L::kVAtom + (kk & 3) * 32) >> 4),
                    id_o, (j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(pv_done);
           mma_commit(v_empty(j & 1));
@@ -257,146 +348,153 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       }
       __syncwarp();
     }
-  } else if (warp < 8) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax
-    regs_inc<kRegsSoftmax>();
-    const int quarter = warp & 3, r = quarter * 32 + lane, row = row0 + r;
-    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kColO;
+    const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, row = row0 + r;
+    const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kColO + half * (D / 2);
     const bool real = row < R;
     const int i = min(row, R - 1) / G;
-    float m_used = -INFINITY, l = 0.f, c_row = 0.f;
-    int E = -1000;  // exponent that O is relative to
+    float m_used = -INFINITY, l = 0.f, c = 0.f;
     uint32_t nan_groups = 0;
-    bool ok = n > 0 && warp_wait(q_full, 0, err, kErrWaitLoad, abort_flag);
+    bool ok = n > 0;
     if (ok) {
-      c_row = reinterpret_cast<const float*>(smem + L::kRow)[r];
-      // the row's sums of q for the product of depth 16: per group hi hi lo lo,
-      // against m + 8 s as hi lo hi lo (2^8 moved from one to the other: fp16's range)
-      uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      c = reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK);
+      if (half == 0) {
+        // the row's sums of q for the product of depth 16: per group hi hi lo lo,
+        // against m + 8 s as hi lo hi lo (a factor of 4 moved over: fp16's range)
+        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int gg = 0; gg < NG; ++gg) {
-        const float q = reinterpret_cast<const float*>(smem + L::kQs)[r * NG + gg] * 0x1p-8f;
-        const float hi = __half2float(__float2half_rn(q));
-        x[2 * gg] = pack_half2(hi, hi);
-        x[2 * gg + 1] = pack_half2(q - hi, q - hi);
+        for (int gg = 0; gg < NG; ++gg) {
+          const float q = reinterpret_cast<const float*>(smem + L::kQs)[r * NG + gg] * 0.25f;
+          const float hi = __half2float(__float2half_rn(q));
+          x[2 * gg] = pack_half2(hi, hi);
+          x[2 * gg + 1] = pack_half2(q - hi, q - hi);
+        }
+        tmem_st8(t_lane + kColQx, x);
+        tmem_st_wait();
+        fence_before_sync();
       }
-      tmem_st8(t_lane + kColQx, x);
-      tmem_st_wait();
-      fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(qx_full);
     }
-    for (int j = 0; ok && j < n; ++j) {
-      if (!(ok = warp_spin_wait(s_full(j & 1), (j >> 1) & 1, err, kErrWaitAcc, abort_flag))) break;
-      // V's exponent and poison words come with v_full
-      if (!(ok = warp_wait(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag))) break;
+    for (int j = 0; j < n; ++j) {
+      if (ok) ok = warp_wait(s_full(j & 1), (j >> 1) & 1, err, kErrWaitAcc, abort_flag);
       fence_after_sync();
-      const uint32_t t_s = t_lane + col_s(j & 1);
-      const float c = c_row * exp2i(exp_k[j & 3]);
-      const int eV = exp_v[j & 3];
-      uint32_t sv[128];
-      tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-      tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-      tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
-      tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-      tmem_ld_wait();
+      const uint32_t t_s = t_lane + col_s(j & 1) + half * 64;
       const int v0 = (t_begin + j) * 4;
       bool full = v0 + 4 <= vis.count() && vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= vis.L;
       if (a.window)
         full = full && ((long long)vis.block(v0) * kQ4Tokens > (long long)vis.L + i_last - a.window ||
                         vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= a.n_sink);
-      if (!full) {
+      // V's poison words come with its tile
+      if (ok && !full) ok = warp_wait(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag);
+      if (!full) {  // hidden columns of S become -inf in tensor memory
         const long long from = a.window ? (long long)vis.L + i - a.window + 1 : 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          // the block's tokens that the row sees, as a mask over its slots
-          uint32_t seen = 0;
-          const bool there = v0 + b < vis.count();
-          const int t0 = there ? vis.block(v0 + b) * kQ4Tokens : 0;
-#pragma unroll
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+          const int vb = v0 + half * 2 + b;
+          const int t0 = vb < vis.count() ? vis.block(vb) * kQ4Tokens : 0x40000000;
+          uint32_t seen = 0;  // slots of the block that the row sees
+#pragma unroll 1
           for (int q = 0; q < 32; ++q) {
             const int tok = t0 + ((q & 7) >> 2) * 16 + ((q >> 1) & 1) * 8 + (q >> 3) * 2 + (q & 1);
-            const bool see = there && tok < vis.L && (tok >= from || tok < a.n_sink);
-            if (see) seen |= 1u << q;
-            else sv[b * 32 + q] = __float_as_uint(-INFINITY);
+            if (tok < vis.L && (tok >= from || tok < a.n_sink)) seen |= 1u << q;
           }
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg)
-            if (seen & poison[((j & 3) * NG + gg) * 4 + b]) nan_groups |= 1u << gg;
+            if (seen & poison[((j & 3) * NG + gg) * 4 + half * 2 + b]) nan_groups |= 1u << gg;
+          uint32_t sv[32];
+          tmem_ld32(t_s + b * 32, sv);
+          tmem_ld_wait_dep(sv);
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            if (!(seen >> q & 1)) sv[q] = __float_as_uint(-INFINITY);
+          tmem_st32(t_s + b * 32, sv);
         }
+        tmem_st_wait();
       }
-      float m8[8];
+      // S is read twice, 32 columns at a time (for the maximum, for the weights),
+      // in loops that stay rolled: six roles share the instruction caches
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int b = 0; b < 2; ++b) {
+        uint32_t sv[32];
+        tmem_ld32(t_s + b * 32, sv);
+        tmem_ld_wait_dep(sv);
 #pragma unroll
-      for (int q8 = 0; q8 < 8; ++q8) {
-        m8[q8] = __uint_as_float(sv[16 * q8]);
+        for (int q4 = 0; q4 < 4; ++q4)
 #pragma unroll
-        for (int jj = 1; jj < 15; jj += 2)
-          m8[q8] = max3f(m8[q8], __uint_as_float(sv[16 * q8 + jj]), __uint_as_float(sv[16 * q8 + jj + 1]));
-        m8[q8] = fmaxf(m8[q8], __uint_as_float(sv[16 * q8 + 15]));
+          for (int jj = 0; jj < 8; jj += 2)
+            m4[q4] = max3f(m4[q4], __uint_as_float(sv[8 * q4 + jj]), __uint_as_float(sv[8 * q4 + jj + 1]));
       }
-      const float mx = fmaxf(fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5])), fmaxf(m8[6], m8[7]));
-      const float m_new = fmaxf(m_used, mx * c);
-      const bool raise = m_new > m_used + kRaise;
-      if (__any_sync(0xffffffffu, raise) || eV > E) {
+      const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]) * c;
+      // both halves learn whether one of them asks for a raise, or gave up
+      if (named_bar_red_or(3, 256, !ok || mx > m_used + kRaise)) {
+        half_max[half * 128 + r] = mx;
+        if (named_bar_red_or(3, 256, !ok)) break;
+        const float m_new = fmaxf(m_used, fmaxf(mx, half_max[(half ^ 1) * 128 + r]));
+        const bool raise = m_new > m_used + kRaise;
         const float f = raise ? ex2_approx(m_used - m_new) : 1.f;
         l *= f;
+        if (raise) m_used = m_new;
         if (j > 0) {
           // O must hold every earlier tile's P V
-          if (!(ok = warp_wait(pv_done, (j - 1) & 1, err, kErrWaitAcc, abort_flag))) break;
+          if (!(ok = warp_wait(pv_done, (j - 1) & 1, err, kErrWaitAcc, abort_flag))) continue;
           fence_after_sync();
-          const float fo = eV > E ? f * exp2i(max(E - eV, -126)) : f;
-#pragma unroll
-          for (int c0 = 0; c0 < D / 32; ++c0) {
+          for (int c0 = 0; c0 < D / 64; ++c0) {
             uint32_t v[32];
             tmem_ld32(t_o + c0 * 32, v);
-            tmem_ld_wait();
+            tmem_ld_wait_dep(v);
 #pragma unroll
-            for (int jj = 0; jj < 32; ++jj) v[jj] = __float_as_uint(__uint_as_float(v[jj]) * fo);
+            for (int jj = 0; jj < 32; ++jj) v[jj] = __float_as_uint(__uint_as_float(v[jj]) * f);
             tmem_st32(t_o + c0 * 32, v);
           }
           tmem_st_wait();
         }
-        if (raise) m_used = m_new;
-        E = max(E, eV);
       }
       const float ref = m_used == -INFINITY ? 0.f : m_used;
-      const int shift = max(eV - E + kPShift, -40);  // beyond: 2^-40 of the largest value, l stays exact
-      const float bias = (float)shift - ref;
+      const float bias = (float)kPShift - ref;
       const float2 c2 = make_float2(c, c), b2 = make_float2(bias, bias);
       float2 ls = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int c0 = 0; c0 < 4; ++c0) {
-        uint32_t pk[16];
+#pragma unroll 1
+      for (int c0 = 0; c0 < 2; ++c0) {
+        uint32_t pk[16], sv[32];
+        tmem_ld32(t_s + c0 * 32, sv);
+        tmem_ld_wait_dep(sv);
 #pragma unroll
         for (int jj = 0; jj < 16; ++jj) {
-          const float2 t = ffma2(make_float2(__uint_as_float(sv[c0 * 32 + 2 * jj]), __uint_as_float(sv[c0 * 32 + 2 * jj + 1])),
-                                 c2, b2);
+          const float2 t = ffma2(make_float2(__uint_as_float(sv[2 * jj]), __uint_as_float(sv[2 * jj + 1])), c2, b2);
           const float2 pp = make_float2(ex2_approx(t.x), ex2_approx(t.y));
           ls = fadd2(ls, pp);
           pk[jj] = pack_half2(pp.x, pp.y);
         }
-        tmem_st16(t_s + c0 * 16, pk);
+        tmem_st16(t_s + c0 * 16, pk);  // over this half's own columns of S
       }
       tmem_st_wait();
-      l = fmaf(ls.x + ls.y, exp2i(-shift), l);
+      l += ls.x + ls.y;
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(j & 1));
     }
     if (ok) ok = warp_wait(o_done, 0, err, kErrWaitAcc, abort_flag);
     ok = ok && !*abort_flag;
+    // l of the row's two halves
+    half_max[half * 128 + r] = l;
+    named_bar_sync(3, 256);
+    l += half_max[(half ^ 1) * 128 + r];
     const long long at = ((long long)blockIdx.x * 128 + r);
+    float* po = p.part_o + at * D + half * (D / 2);
     if (ok) {
       fence_after_sync();
-      const float back = exp2i(min(max(E - kPShift, -126), 127));
+      const float back = exp2i(eV - kPShift);
 #pragma unroll
-      for (int c0 = 0; c0 < D / 32; ++c0) {
+      for (int c0 = 0; c0 < D / 64; ++c0) {
         uint32_t v[32];
         tmem_ld32(t_o + c0 * 32, v);
-        tmem_ld_wait();
-        const float add = (nan_groups >> (c0 / 2) & 1) ? NAN : 0.f;
+        tmem_ld_wait_dep(v);
+        const float add = (nan_groups >> ((half * (D / 2) + c0 * 32) / kQ4Group) & 1) ? NAN : 0.f;
         if (real) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + c0 * 32);
+          float4* dst = reinterpret_cast<float4*>(po + c0 * 32);
 #pragma unroll
           for (int q4 = 0; q4 < 8; ++q4)
             dst[q4] = make_float4(fmaf(__uint_as_float(v[4 * q4]), back, add), fmaf(__uint_as_float(v[4 * q4 + 1]), back, add),
@@ -404,165 +502,110 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
         }
       }
     } else if (real) {  // no tiles (or an abandoned call): nothing to add
-      for (int d = 0; d < D; d += 4) *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int d = 0; d < D / 2; d += 4) *reinterpret_cast<float4*>(po + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (real) *reinterpret_cast<float2*>(p.part_ml + at * 2) = ok ? make_float2(m_used, l) : make_float2(-INFINITY, 0.f);
-  } else {
-    // --------------------------------------------- dequantise: K or V
-    regs_dec<kRegsDequant>();
-    const bool is_v = warp >= 12;
+    if (real && half == 0)
+      *reinterpret_cast<float2*>(p.part_ml + at * 2) = ok ? make_float2(m_used, l * exp2i(-kPShift)) : make_float2(-INFINITY, 0.f);
+  } else if (warp < 16) {
+    // ------------------------------------------------------- dequantise K
     const int w4 = warp & 3, tid = w4 * 32 + lane;
-    if (!is_v) {
-      // Q: thread = row, scaled by a power of two, channels of a chunk in field order
-      const int row = row0 + tid;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                               (((long long)s * a.n + min(row, R - 1) / G) * a.Hq + g * G + min(row, R - 1) % G) * D;
-      float top = 0.f;
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(xs[e] << 16)), fabsf(__uint_as_float(xs[e] & 0xffff0000u))));
-      }
-      int ex = (int)(__float_as_uint(top) >> 23);
-      ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, 12);
-      const float up = __uint_as_float((uint32_t)(264 - ex) << 23), down = __uint_as_float((uint32_t)(ex - 10) << 23);
-      reinterpret_cast<float*>(smem + L::kRow)[tid] = down * a.scale_log2;
-      float sum[NG];
-#pragma unroll
-      for (int gg = 0; gg < NG; ++gg) sum[gg] = 0.f;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + c);
-        const float y[8] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                            __uint_as_float(x.y & 0xffff0000u), __uint_as_float(x.z << 16),
-                            __uint_as_float(x.z & 0xffff0000u), __uint_as_float(x.w << 16),
-                            __uint_as_float(x.w & 0xffff0000u)};
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
-        if (row < R)
-          o = make_uint4(pack_half2(y[q4_k_channel(0, 0)] * up, y[q4_k_channel(0, 1)] * up),
-                         pack_half2(y[q4_k_channel(1, 0)] * up, y[q4_k_channel(1, 1)] * up),
-                         pack_half2(y[q4_k_channel(2, 0)] * up, y[q4_k_channel(2, 1)] * up),
-                         pack_half2(y[q4_k_channel(3, 0)] * up, y[q4_k_channel(3, 1)] * up));
-        *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kAtom + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = o;
-        sum[c >> 3] += (((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]))) * up;
-      }
-#pragma unroll
-      for (int gg = 0; gg < NG; ++gg) reinterpret_cast<float*>(smem + L::kQs)[tid * NG + gg] = row < R ? sum[gg] : 0.f;
-      for (int b = 0; b < 2; ++b)  // the unused half of the depth-16 rows
-        *reinterpret_cast<uint4*>(smem + L::kKx + b * 4096 + 2048 + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
-    // this thread's slot of a tile: block w4, slot lane
+    // this thread's row of a tile is slot `lane` of block w4
     const int f_of = (lane & 7) >> 1, tig_of = lane >> 3, half_of = lane & 1;
-    const int tok_of = (f_of >> 1) * 16 + (f_of & 1) * 8 + tig_of * 2 + half_of;  // its token in the block
-    float* wmax = maxima + (is_v ? 8 : 0);
-    const int bar_id = is_v ? 2 : 1;
+    const int tok_of = (f_of >> 1) * 16 + (f_of & 1) * 8 + tig_of * 2 + half_of;
+    // the lanes of eight slots read different 16-byte chunks (tig = x ^ it), so
+    // that neither loads nor stores meet a bank twice: x = 0 2 3 1 for f = 0..3
+    const int x_of = ((f_of ^ (f_of >> 1)) & 1) << 1 | f_of >> 1;
+    const float norm = exp2i(-eK);
     for (int j = 0; j < n; ++j) {
       const int sl = j % kRaw, b2 = j & 1;
-      bool ok = warp_wait(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag);
-      if (ok) ok = warp_wait(is_v ? v_empty(b2) : k_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag);
-      const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile;
-      // scales of this thread's token; 0 where no row of the tile sees it
-      const int vb = (t_begin + j) * 4 + w4;
-      const int tok = vb < vis.count() ? vis.block(vb) * kQ4Tokens + tok_of : 0x7fffffff;
-      const bool keep = !a.window || tok < a.n_sink;
-      const bool some = ok && tok < vis.L && (keep || (long long)tok > (long long)vis.L + i_first - a.window);
-      const bool every = keep || (long long)tok > (long long)vis.L + i_last - a.window;
-      float sc[NG], mid[NG], top = 0.f;
-      uint32_t bad = 0;
+      // the row scales and sums of q lie in the second K tile until they are read
+      if (j == 1 && !warp_wait(qx_full, 0, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait(k_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
+      const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
+      const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);
+      uint32_t s2[NG], x[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int gg = 0; gg < NG; ++gg) {
-        sc[gg] = mid[gg] = 0.f;
-        if (some) {
-          const uint32_t sm = reinterpret_cast<const uint32_t*>(raw + w4 * B::kBytes + (is_v ? B::kVs : B::kKs))[tok_of * NG + gg];
-          sc[gg] = q4_scale(sm);
-          mid[gg] = fmaf(sc[gg], 8.f, q4_min(sm));
-          if (is_v && !every && sc[gg] != sc[gg]) {  // rows that see it become NaN in the softmax
-            sc[gg] = mid[gg] = 0.f;
-            bad |= 1u << gg;
-          }
-          top = fmaxf(top, fmaf(sc[gg], 8.f, fabsf(mid[gg])));
-        }
+        const uint32_t sm = reinterpret_cast<const uint32_t*>(raw + B::kKs)[tok_of * NG + gg];
+        const float sc = t.some ? q4_scale(sm) * norm : 0.f;
+        const float y = t.some ? fmaf(q4_scale(sm), 8.f, q4_min(sm)) * norm * 4.f : 0.f;
+        const float hi = __half2float(__float2half_rn(y));
+        s2[gg] = pack_half2(sc, sc);
+        x[2 * gg] = x[2 * gg + 1] = pack_half2(hi, y - hi);
       }
+      *reinterpret_cast<uint4*>(smem + L::kKx + b2 * 4096 + tid * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+      const uint8_t* kr = raw + tok_of * B::kRow;
+      uint8_t* dst = smem + L::kK + b2 * L::kTile + tid * 128;
+#pragma unroll 1
+      for (int it = 0; it < 4; ++it) {
+        const int tig = x_of ^ it;
+        uint32_t w[D / 32];
+        if (D == 128) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kr + tig * 16);
+        else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(kr + tig * 8);
 #pragma unroll
-      for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      if (lane == 0) wmax[b2 * 4 + w4] = top;
-      if (is_v) {
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          const uint32_t word = __ballot_sync(0xffffffffu, bad >> gg & 1);
-          if (lane == 0) poison[((j & 3) * NG + gg) * 4 + w4] = word;
-        }
-      }
-      if (named_bar_red_or(bar_id, 128, !ok)) break;  // a warp gave up: all leave
-      top = fmaxf(fmaxf(wmax[b2 * 4], wmax[b2 * 4 + 1]), fmaxf(wmax[b2 * 4 + 2], wmax[b2 * 4 + 3]));
-      // the tile's largest magnitude into [1, 2)
-      const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 120);
-      const float norm = exp2i(-e);
-      if (tid == 0) (is_v ? exp_v : exp_k)[j & 3] = e;
-      if (!is_v) {
-        uint32_t s2[NG], x[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          s2[gg] = pack_half2(sc[gg] * norm, sc[gg] * norm);
-          const float y = mid[gg] * norm * 0x1p8f, hi = __half2float(__float2half_rn(y));
-          x[2 * gg] = x[2 * gg + 1] = pack_half2(hi, y - hi);
-        }
-        *reinterpret_cast<uint4*>(smem + L::kKx + b2 * 4096 + tid * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-        // row = slot; the four lanes of a slot pair of eight read different
-        // 16-byte chunks (tig = x ^ i), so loads and stores meet no bank twice
-        const int x_of = ((f_of ^ (f_of >> 1)) & 1) << 1 | f_of >> 1;  // 0 2 3 1 for f = 0..3
-        const uint8_t* kr = raw + w4 * B::kBytes + tok_of * B::kRow;
-        uint8_t* dst = smem + L::kK + b2 * L::kTile + tid * 128;
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const int tig = x_of ^ it;
-          uint32_t w[D / 32];
-          if (D == 128) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(kr + tig * 16);
-          else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(kr + tig * 8);
-#pragma unroll
-          for (int ww = 0; ww < D / 32; ++ww) {
-            const int gg = ww >> 1;
-            const uint4 o = make_uint4(dequant<0>(w[ww], s2[gg]), dequant<1>(w[ww], s2[gg]), dequant<2>(w[ww], s2[gg]),
-                                       dequant<3>(w[ww], s2[gg]));
-            *reinterpret_cast<uint4*>(dst + gg * L::kAtom + (((tig * 2 + (ww & 1)) ^ (tid & 7)) << 4)) = o;
-          }
-        }
-      } else {
-        // scales by (block, tig, group, field): a word's eight tokens
-        __half* tab = reinterpret_cast<__half*>(smem + L::kTab);
-#pragma unroll
-        for (int gg = 0; gg < NG; ++gg) {
-          __half* t = tab + (((w4 * 4 + tig_of) * NG + gg) * 4 + f_of) * 4 + half_of;
-          t[0] = __float2half_rn(sc[gg] * norm);
-          t[2] = __float2half_rn(mid[gg] * norm);
-        }
-        named_bar_sync(bar_id, 128);
-        const int d = tid % D, x_of = (d >> 1) & 3;
-        uint8_t* dst = smem + L::kV + b2 * 2 * L::kVAtom + d * 128;
-#pragma unroll
-        for (int bb = 0; bb < 4 * D / 128; ++bb) {
-          const int b = (tid / D) * 2 + bb;  // D = 64: two threads share a channel
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int tig = x_of ^ it;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(raw + b * B::kBytes + B::kV + q4_v_word(d, tig));
-            const uint4* t = reinterpret_cast<const uint4*>(tab + ((b * 4 + tig) * NG + d / kQ4Group) * 16);
-            const uint4 t0 = t[0], t1 = t[1];
-            const uint4 o = make_uint4(dequant<0>(w, t0.x, t0.y), dequant<1>(w, t0.z, t0.w), dequant<2>(w, t1.x, t1.y),
-                                       dequant<3>(w, t1.z, t1.w));
-            *reinterpret_cast<uint4*>(dst + (b >> 1) * L::kVAtom + ((((b & 1) * 4 + tig) ^ (d & 7)) << 4)) = o;
-          }
+        for (int ww = 0; ww < D / 32; ++ww) {
+          const int gg = ww >> 1;
+          *reinterpret_cast<uint4*>(dst + gg * L::kAtom + (((tig * 2 + (ww & 1)) ^ (tid & 7)) << 4)) =
+              make_uint4(dequant<0>(w[ww], s2[gg]), dequant<1>(w[ww], s2[gg]), dequant<2>(w[ww], s2[gg]),
+                         dequant<3>(w[ww], s2[gg]));
         }
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(is_v ? v_full(b2) : k_full(b2));
+        mbar_arrive(k_full(b2));
+        mbar_arrive(raw_empty(sl));
+      }
+    }
+  } else {
+    // ------------------------------------------------------- dequantise V
+    // A thread prepares the scales of one slot (block w4, slot lane), then takes
+    // the words of one tig of its warp's block: channels 8 j + sub.
+    const int w4 = warp & 3;
+    const int f_of = (lane & 7) >> 1, tig_of = lane >> 3, half_of = lane & 1;
+    const int tok_of = (f_of >> 1) * 16 + (f_of & 1) * 8 + tig_of * 2 + half_of;
+    // lanes of eight stores: four tigs, two channels 4 apart: eight different chunks
+    const int tig = lane & 3, sub = (lane >> 2 & 1) * 4 + (lane >> 3);
+    const float norm = exp2i(-eV);
+    for (int j = 0; j < n; ++j) {
+      const int sl = j % kRaw, b2 = j & 1;
+      if (!warp_wait(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait(v_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
+      const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
+      uint8_t* tab = smem + L::kTab + w4 * (4 * NG * 32);  // [tig][group][f] (s pair, m + 8 s pair) of the warp's block
+      const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);
+#pragma unroll
+      for (int gg = 0; gg < NG; ++gg) {
+        const uint32_t sm = reinterpret_cast<const uint32_t*>(raw + B::kVs)[tok_of * NG + gg];
+        float sc = q4_scale(sm), mid = fmaf(sc, 8.f, q4_min(sm));
+        // poisoned and seen by some rows only: those become NaN in the softmax
+        const bool bad = t.some && !t.every && sc != sc;
+        if (!t.some || bad) sc = mid = 0.f;
+        const uint32_t word = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) poison[((j & 3) * NG + gg) * 4 + w4] = word;
+        __half* x = reinterpret_cast<__half*>(tab) + ((tig_of * NG + gg) * 4 + f_of) * 4 + half_of;
+        x[0] = __float2half_rn(sc * norm);
+        x[2] = __float2half_rn(mid * norm);
+      }
+      __syncwarp();
+      uint8_t* dst = smem + L::kV + b2 * 2 * L::kVAtom + (w4 >> 1) * L::kVAtom + sub * 128 + ((((w4 & 1) * 4 + tig) ^ sub) << 4);
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        const uint4 w = *reinterpret_cast<const uint4*>(raw + B::kV + c * 512 + (sub * 4 + tig) * 16);
+        const uint4* x = reinterpret_cast<const uint4*>(tab + (tig * NG + c / 2) * 32);
+        const uint4 t0 = x[0], t1 = x[1];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(dst + (c * 4 + e) * 1024) =
+              make_uint4(dequant<0>(ws[e], t0.x, t0.y), dequant<1>(ws[e], t0.z, t0.w), dequant<2>(ws[e], t1.x, t1.y),
+                         dequant<3>(ws[e], t1.z, t1.w));
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(v_full(b2));
         mbar_arrive(raw_empty(sl));
       }
     }

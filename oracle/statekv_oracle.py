@@ -438,18 +438,20 @@ def window_attention(q, k, v, past_k=None, past_v=None, window: int = 0, n_sink:
     pos = np.arange(L + n)
     out, mass = np.empty((n, Hq, d)), np.empty((n, Hq, d))
     lse, span = np.empty((Hq, n)), np.empty((Hq, n))
-    for i in range(n):
-        see = pos <= L + i
-        if window:
-            see &= (pos > L + i - window) | (pos < n_sink)
-        for h in range(Hq):
-            g = kv_head_of(h, Hq, Hkv)
-            kk, vv = k[see, g], v[see, g]
-            a = kk @ q[i, h] / np.sqrt(d)
-            top = a.max()
-            w = np.exp(a - top)
-            lse[h, i] = top + np.log(w.sum())
-            w /= w.sum()
-            out[i, h], mass[i, h] = w @ vv, w @ np.abs(vv)
-            span[h, i] = (np.abs(kk) @ np.abs(q[i, h])).max() / np.sqrt(d)
+    at = (L + np.arange(n))[:, None]
+    see = pos <= at
+    if window:
+        see &= (pos > at - window) | (pos < n_sink)
+    for h in range(Hq):
+        g = kv_head_of(h, Hq, Hkv)
+        used = see.any(0)                   # positions that some token sees
+        kk, vv, s = k[used, g], v[used, g], see[:, used]
+        a = np.where(s, q[:, h] @ kk.T / np.sqrt(d), -np.inf)
+        top = a.max(1, keepdims=True)
+        w = np.exp(a - top)
+        total = w.sum(1, keepdims=True)
+        lse[h] = (top + np.log(total))[:, 0]
+        w /= total
+        out[:, h], mass[:, h] = w @ vv, w @ np.abs(vv)
+        span[h] = np.where(s, np.abs(q[:, h]) @ np.abs(kk).T, 0.0).max(1) / np.sqrt(d)
     return out, lse, mass, span

@@ -209,6 +209,9 @@ DECODE = [
     (1, 7, 1, 128, 640, 30, 64, 1),
     (1, 7, 1, 128, 640, 30, 10, 0),       # text tokens that see no cached one
     (1, 130, 1, 64, 100, 1, 0, 0),        # 130 query heads on one KV head
+    (1, 48, 12, 64, 5000, 17, 0, 0),      # several key tiles per block of the 128-row kernel
+    (1, 40, 10, 128, 6007, 20, 0, 0),
+    (2, 60, 20, 64, 3001, 9, 2000, 40),
 ]
 
 
