@@ -110,8 +110,7 @@ cudaError_t launch_attn_combine(const AttnTcArgs& a, int d, cudaStream_t st, boo
 cudaError_t launch_attn_merge_wide(const AttnTcArgs& a, int d, int n_sm, cudaStream_t st, bool pdl = false);
 MergeArgs merge_args(const AttnTcArgs& a, int d);
 
-// 4-bit cache: append and read back; attention over it (and, with no cache, over
-// a sequence alone) on the CUDA cores.
+// 4-bit cache: append and read back.
 cudaError_t launch_q4_append(Q4IoArgs a, int dtype, int d, cudaStream_t st, bool pdl = false);
 cudaError_t launch_q4_read(Q4IoArgs a, int dtype, int d, cudaStream_t st);
 // Attention over the cache: how a call is split, and the bytes of its workspace.
@@ -124,8 +123,10 @@ cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspac
 // Its kernel for 128-row tiles (tensor cores), and the first error its waits recorded.
 cudaError_t launch_q4_attn_tc(const Q4AttnArgs& p, int d, cudaStream_t st);
 cudaError_t q4_attn_tc_status(int* code);
-cudaError_t launch_window_simt(const WindowArgs& a, int dtype, int d, cudaStream_t st);
-// The same without a cache on the tensor cores (bf16, window >= 1), and the first error its waits recorded.
+
+// Causal attention of a sequence with a window (>= 1) and first tokens: float32 on
+// the CUDA cores, bf16 on the tensor cores, and the first error the latter's waits recorded.
+cudaError_t launch_window_simt(const WindowArgs& a, int d, cudaStream_t st);
 cudaError_t launch_window_tc(const WindowArgs& a, int d, cudaStream_t st);
 cudaError_t window_tc_status(int* code);
 

@@ -236,7 +236,7 @@ int sink_window_prefill_batched(const void* q, const void* k, const void* v, int
   if (n_sink < 0) return fail(STATEKV_ERR_INVALID_ARG, "n_sink=%d must not be negative", n_sink);
   if (n_seq > 65535 || Hq > 65535 || n_tokens > (1 << 24))
     return fail(STATEKV_ERR_UNSUPPORTED, "n_seq=%d, Hq=%d or n_tokens=%d too large", n_seq, Hq, n_tokens);
-  if ((long long)n_seq * Hq * ((n_tokens + 127ll) / 128) > 0x7fffffffll)
+  if ((long long)n_seq * Hq * ((n_tokens + 63ll) / 64) > 0x7fffffffll)
     return fail(STATEKV_ERR_UNSUPPORTED, "n_seq=%d x Hq=%d x n_tokens=%d is too large", n_seq, Hq, n_tokens);
   if (n_tokens == 0) return STATEKV_OK;
   if (!q || !k || !v || !out) return fail(STATEKV_ERR_INVALID_ARG, "null pointer");
@@ -262,7 +262,7 @@ int sink_window_prefill_batched(const void* q, const void* k, const void* v, int
   a.n_sink = n_sink;
   a.scale_log2 = skv::kLog2e / sqrtf((float)d);
   const cudaError_t e = dtype == STATEKV_BF16 ? skv::launch_window_tc(a, d, static_cast<cudaStream_t>(stream))
-                                              : skv::launch_window_simt(a, dtype, d, static_cast<cudaStream_t>(stream));
+                                              : skv::launch_window_simt(a, d, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return fail(STATEKV_ERR_CUDA, "sink_window_prefill launch failed: %s", cudaGetErrorString(e));
   return STATEKV_OK;

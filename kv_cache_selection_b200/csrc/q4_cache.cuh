@@ -78,14 +78,8 @@ __host__ __device__ __forceinline__ constexpr int q4_half_of(int n) { return 0x7
 __host__ __device__ __forceinline__ constexpr int q4_k_channel(int f, int half) {
   return (half ? 0x3465 : 0x7021) >> (4 * f) & 7;
 }
-// Eight nibbles -> word, and nibble n of a word.
+// Eight nibbles -> word.
 __device__ __forceinline__ uint32_t q4_rotate(uint32_t nibbles) { return __funnelshift_l(nibbles, nibbles, 2); }
-__device__ __forceinline__ int q4_nibble(uint32_t x, int n) { return (int)(__funnelshift_r(x, x, 2) >> (4 * n) & 15u); }
-// Nibble of the V word that holds block token t.
-__device__ __forceinline__ int q4_v_nibble(int t) {
-  const int f = (t >> 4) * 2 + ((t >> 3) & 1);
-  return (t & 1) ? (0x3465 >> (4 * f) & 7) : (0x7021 >> (4 * f) & 7);
-}
 
 __device__ __forceinline__ float q4_scale(uint32_t sm) { return __uint_as_float(sm << 16); }
 __device__ __forceinline__ float q4_min(uint32_t sm) { return __uint_as_float(sm & 0xffff0000u); }

@@ -10,7 +10,9 @@ library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import threading
 
 import torch
 
@@ -322,34 +324,36 @@ def full_causal_prefill(q, k, v, out=None, lse=None, with_lse=True, stream=None)
     return out, lse
 
 
-class _device:
-    """Makes a tensor's device the current one for a call (nothing to do where
-    it already is)."""
-
-    __slots__ = ("dev", "back")
-
-    def __init__(self, dev):
-        self.dev, self.back = dev, -1
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.dev:
-            torch.cuda.set_device(self.dev)
-            self.back = now
-
-    def __exit__(self, *exc):
-        if self.back >= 0:
-            torch.cuda.set_device(self.back)
+def _on(dev):
+    """Makes a tensor's device the current one; returns the device to go back
+    to, or -1 where it already was."""
+    now = torch.cuda.current_device()
+    if now == dev:
+        return -1
+    torch.cuda.set_device(dev)
+    return now
 
 
-def _empty(shape, dtype, dev, stream):
-    """A new tensor for work on `stream` (allocated for that stream, so that
-    its memory is not still in use by work queued elsewhere)."""
+def _back(dev):
+    if dev >= 0:
+        torch.cuda.set_device(dev)
+
+
+@functools.lru_cache(maxsize=None)
+def _float32_on(device):
+    """A float32 tensor on the device, to make others like it."""
+    return torch.empty((), dtype=torch.float32, device=device)
+
+
+def _empty(like, shape, stream):
+    """A new tensor of like's type and device for work on `stream` (allocated
+    for that stream, so that its memory is not still in use by work queued
+    elsewhere)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_ptr(stream), device=dev)
+        return like.new_empty(shape)
+    st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream_ptr(stream), device=like.device)
     with torch.cuda.stream(st):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape)
 
 
 class Q4Cache:
@@ -369,28 +373,35 @@ class Q4Cache:
         self.Hkv, self.d, self.capacity, self.S = Hkv, d, capacity, n_streams
         self.data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
         self._dev = self.data.get_device()
-        self._ws_bytes = {}
+        self._ptr = self.data.data_ptr()
+        self._proto = {t: torch.empty((), dtype=t, device=self.data.device) for t in (torch.bfloat16, torch.float32)}
+        # workspaces of decodes on the current stream, by stream and size: one
+        # call at a time uses them (the lock), in the stream's order
+        self._ws, self._ws_bytes, self._lock = {}, {}, threading.Lock()
 
-    def _tokens(self, t, heads, name, dtype, n=None):
-        """Checks a [(S,) n, heads, d] tensor; returns its n."""
+    def _need(self, t, heads, name, dtype, n=None):
+        """Checks a [(S,) n, heads, d] tensor on the cache's device; returns its n."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        lead = (self.S,) if t.dim() == 4 or self.S != 1 else ()
+        shape = t.shape
         if n is None:
-            n = t.shape[-3] if t.dim() >= 3 else 0
-        _need(t, lead + (n, heads, self.d), dtype, name)
-        self._same_device(t, name)
+            n = shape[-3] if len(shape) >= 3 else 0
+        if not (t.get_device() == self._dev >= 0 and t.dtype is dtype and t.is_contiguous()
+                and (shape == (self.S, n, heads, self.d) or (self.S == 1 and shape == (n, heads, self.d)))):
+            lead = (self.S,) if t.dim() == 4 or self.S != 1 else ()
+            _need(t, lead + (n, heads, self.d), dtype, name)
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.data.device}")
         return n
 
-    def _same_device(self, t, name):
+    def _need_like(self, t, shape, dtype, name):
+        _need(t, shape, dtype, name)
         if t.get_device() != self._dev:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.data.device}")
 
     def _at(self, at, name):
         """(host value, device pointer) of a token number or an int32 [S] tensor."""
         if isinstance(at, torch.Tensor):
-            _need(at, (self.S,), torch.int32, name)
-            self._same_device(at, name)
+            self._need_like(at, (self.S,), torch.int32, name)
             return 0, at.data_ptr()
         return int(at), None
 
@@ -398,15 +409,18 @@ class Q4Cache:
         """Quantise k, v [(S,) n, Hkv, d] into cache tokens start .. start+n-1
         (start: a number, or int32 [S] on the device for a start per stream,
         where tokens outside the cache are dropped)."""
-        code = _dtype_code(k.dtype)
-        n = self._tokens(k, self.Hkv, "k", k.dtype)
-        _need(v, k.shape, k.dtype, "v")
-        self._same_device(v, "v")
+        dt = k.dtype
+        code = _dtype_code(dt)
+        n = self._need(k, self.Hkv, "k", dt)
+        self._need(v, self.Hkv, "v", dt, n)
         host, dev = self._at(start, "start")
-        with _device(self._dev):
-            _check(lib.statekv_q4_append(self.data.data_ptr(), self.S, self.Hkv, self.d, self.capacity,
-                                         k.data_ptr(), v.data_ptr(), n, code, host, dev,
-                                         _stream_ptr(stream, self._dev)))
+        back = _on(self._dev)
+        try:
+            rc = lib.statekv_q4_append(self._ptr, self.S, self.Hkv, self.d, self.capacity, k.data_ptr(), v.data_ptr(),
+                                       n, code, host, dev, _stream_ptr(stream, self._dev))
+        finally:
+            _back(back)
+        _check(rc)
 
     def read(self, start, n, dtype="bf16", k=None, v=None, stream=None):
         """Keys and values [S][n][Hkv][d] of cache tokens start .. start+n-1
@@ -416,18 +430,24 @@ class Q4Cache:
         dt = _torch_dtype(code)
         shape = (self.S, n, self.Hkv, self.d)
         host, dev = self._at(start, "start")
-        made = []
-        for i, t in enumerate((k, v)):
-            if t is None:
-                t = _empty(shape, dt, self.data.device, stream)
-            else:
-                _need(t, shape, dt, "kv"[i])
-                self._same_device(t, "kv"[i])
-            made.append(t)
-        with _device(self._dev):
-            _check(lib.statekv_q4_read(self.data.data_ptr(), self.S, self.Hkv, self.d, self.capacity, host, dev, n,
-                                       code, made[0].data_ptr(), made[1].data_ptr(), _stream_ptr(stream, self._dev)))
-        return made[0], made[1]
+        if n < 0:
+            raise ValueError(f"negative token count {n}")
+        if k is None:
+            k = _empty(self._proto[dt], shape, stream)
+        else:
+            self._need_like(k, shape, dt, "k")
+        if v is None:
+            v = torch.empty_like(k) if stream is None else _empty(k, shape, stream)
+        else:
+            self._need_like(v, shape, dt, "v")
+        back = _on(self._dev)
+        try:
+            rc = lib.statekv_q4_read(self._ptr, self.S, self.Hkv, self.d, self.capacity, host, dev, n, code,
+                                     k.data_ptr(), v.data_ptr(), _stream_ptr(stream, self._dev))
+        finally:
+            _back(back)
+        _check(rc)
+        return k, v
 
     def decode(self, q, k, v, length, window=0, n_sink=0, out=None, lse=None, with_lse=True, stream=None):
         """Attention of n text tokens over the first `length` cache tokens (a
@@ -435,35 +455,50 @@ class Q4Cache:
         q [(S,) n, Hq, d], k/v [(S,) n, Hkv, d]; with window > 0 a token at
         position p sees positions above p - window and those below n_sink.
         Returns (out, lse [(S,) Hq, n] or None)."""
-        code = _dtype_code(q.dtype)
-        Hq = q.shape[-2]
-        n = self._tokens(q, Hq, "q", q.dtype)
-        self._tokens(k, self.Hkv, "k", q.dtype, n)
-        self._tokens(v, self.Hkv, "v", q.dtype, n)
+        dt = q.dtype
+        code = _dtype_code(dt)
+        shape = q.shape
+        Hq = shape[-2]
+        n = self._need(q, Hq, "q", dt)
+        self._need(k, self.Hkv, "k", dt, n)
+        self._need(v, self.Hkv, "v", dt, n)
         host, dev = self._at(length, "length")
         if out is None:
-            out = _empty(q.shape, q.dtype, q.device, stream)
+            out = torch.empty_like(q) if stream is None else _empty(q, shape, stream)
         else:
-            _need(out, q.shape, q.dtype, "out")
-            self._same_device(out, "out")
-        ls = ((self.S,) if q.dim() == 4 else ()) + (Hq, n)
-        if lse is not None:
-            _need(lse, ls, torch.float32, "lse")
-            self._same_device(lse, "lse")
-        elif with_lse:
-            lse = _empty(ls, torch.float32, q.device, stream)
-        with _device(self._dev):
+            self._need_like(out, shape, dt, "out")
+        if with_lse or lse is not None:
+            ls = (self.S, Hq, n) if len(shape) == 4 else (Hq, n)
+            if lse is None:
+                lse = _empty(self._proto[torch.float32], ls, stream)
+            else:
+                self._need_like(lse, ls, torch.float32, "lse")
+        back = _on(self._dev)
+        try:
             need = self._ws_bytes.get((Hq, n, code))
             if need is None:
                 need = lib.statekv_q4_decode_workspace(self.S, Hq, self.Hkv, self.d, n, code)
                 if need < 0:
                     _check(int(need))
                 self._ws_bytes[(Hq, n, code)] = need
-            ws = _empty((need,), torch.uint8, q.device, stream)
-            _check(lib.statekv_q4_decode(self.data.data_ptr(), self.S, Hq, self.Hkv, self.d, self.capacity,
-                                         q.data_ptr(), k.data_ptr(), v.data_ptr(), n, code, host, dev, window, n_sink,
-                                         out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(),
-                                         need, _stream_ptr(stream, self._dev)))
+            st = _stream_ptr(stream, self._dev)
+            args = (self._ptr, self.S, Hq, self.Hkv, self.d, self.capacity, q.data_ptr(), k.data_ptr(), v.data_ptr(), n,
+                    code, host, dev, window, n_sink, out.data_ptr(), lse.data_ptr() if lse is not None else None)
+            if stream is not None or torch.cuda.is_current_stream_capturing():
+                # a workspace of the call's own: the stream may be anybody's, and
+                # a captured graph keeps its memory to itself
+                ws = _empty(self._proto[torch.bfloat16], (need // 2,), stream)
+                rc = lib.statekv_q4_decode(*args, ws.data_ptr(), need, st)
+            else:
+                with self._lock:
+                    ws = self._ws.get(st)
+                    if ws is None or ws[0] < need:
+                        t = _empty(self._proto[torch.bfloat16], (need // 2,), None)
+                        ws = self._ws[st] = (need, t.data_ptr(), t)
+                    rc = lib.statekv_q4_decode(*args, ws[1], ws[0], st)
+        finally:
+            _back(back)
+        _check(rc)
         return out, lse
 
 
@@ -489,20 +524,25 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
     _need(k, lead + (N, Hkv, d), q.dtype, "k")
     _need(v, lead + (N, Hkv, d), q.dtype, "v")
     if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
-    _need(out, lead + (N, Hq, d), q.dtype, "out")
+        out = _empty(q, q.shape, stream)
+    else:
+        _need(out, lead + (N, Hq, d), q.dtype, "out")
     if lse is None and with_lse:
-        lse = _empty(lead + (Hq, N), torch.float32, q.device, stream)
-    if lse is not None:
+        lse = _empty(q if q.dtype is torch.float32 else _float32_on(q.device), lead + (Hq, N), stream)
+    elif lse is not None:
         _need(lse, lead + (Hq, N), torch.float32, "lse")
     dev = q.get_device()
     for t, name in ((k, "k"), (v, "v"), (out, "out"), (lse, "lse")):
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-    with _device(dev):
-        _check(lib.sink_window_prefill_batched(q.data_ptr(), k.data_ptr(), v.data_ptr(), S, N, Hq, Hkv, d, code,
-                                               window, n_sink, out.data_ptr(),
-                                               lse.data_ptr() if lse is not None else None, _stream_ptr(stream, dev)))
+    back = _on(dev)
+    try:
+        rc = lib.sink_window_prefill_batched(q.data_ptr(), k.data_ptr(), v.data_ptr(), S, N, Hq, Hkv, d, code, window,
+                                             n_sink, out.data_ptr(), lse.data_ptr() if lse is not None else None,
+                                             _stream_ptr(stream, dev))
+    finally:
+        _back(back)
+    _check(rc)
     return out, lse
 
 
