@@ -6,7 +6,13 @@
 // one head) and walks the 128-key tiles that any of its rows sees: the sink
 // tiles, then those from row 0's window to the diagonal.  Per key tile and
 // query tile S = Q K^T goes to tensor memory, a softmax warpgroup (thread =
-// row) turns it into P in place, and O += P V reads P from tensor memory.
+// row) turns it into P in place, and O += P V reads P from tensor memory, each
+// half of its keys as soon as it is there.
+//
+// The S tiles form one sequence q = 0, 1, ... (A and B in turn; A alone where B
+// has no rows) over kS buffers in tensor memory: S(q + kS) is issued right after
+// P V(q).  With d = 64 there is room for three, so that the softmax of a tile
+// never waits for the products of the one before; with d = 128 for two.
 //
 // The running maximum is lazy (raised when a logit exceeds it by more than
 // 2^8); it starts at -inf, so a row whose first tiles are hidden takes its
@@ -29,7 +35,6 @@ namespace skv {
 namespace {
 using namespace tc;
 
-constexpr int kSlots = 4;  // K/V ring slots of one 128-key tile
 constexpr int kThreads = 384;
 // launched at 168 registers a thread; warpgroup 0 drops to 72, the softmax
 // warpgroups rise to 216: 128 x 72 + 256 x 216 = 384 x 168
@@ -42,14 +47,16 @@ __device__ int g_err;
 
 template <int D>
 struct Smem {
+  static constexpr int kS = D == 64 ? 3 : 2;      // S buffers
+  static constexpr int kSlots = D == 64 ? 8 : 4;  // K/V ring slots of one 128-key tile
   static constexpr int kAtoms = D / 64;
   static constexpr int kAtomBytes = 128 * 128;
   static constexpr int kTile = kAtoms * kAtomBytes;  // 128 rows x D bf16
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kTile;
   static constexpr int kBar = kKV + kSlots * kTile;
-  // q[2], kv_full[kSlots], kv_empty[kSlots], s_full[2], p_full[2], o_done[2], done
-  static constexpr int kNumBars = 2 + 2 * kSlots + 7;
+  // q[2], kv_full[kSlots], kv_empty[kSlots], s_full[kS], p_full[kS][2 halves], pv_done[2][even, odd tiles], done
+  static constexpr int kNumBars = 2 + 2 * kSlots + 3 * kS + 5;
   static constexpr int kTmem = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmem + 4;
   static constexpr int kBytes = kAbort + 4;
@@ -57,6 +64,30 @@ struct Smem {
   static constexpr int kAlloc = kBytes + 1024 > 116 * 1024 ? kBytes + 1024 : 116 * 1024;
 };
 
+// Ties loaded registers to a wait before it, so that no use moves above that.
+__device__ __forceinline__ void after_wait(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// The MMA warp runs its loop with all lanes, so that the operands stay warp-uniform
+// registers; one elected lane issues.
+__device__ __forceinline__ void mma_ss_e(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void commit_e(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
+}
 // One row again, from its visible tokens alone; a warp, lane = D/32 channels.
 template <int D>
 __device__ __noinline__ void row_again(const WindowArgs& a, int s, int h, int i) {
@@ -103,14 +134,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // unit -> (stream, pair, KV group, head of the group): the heads that share a
-  // K/V range run next to one another
+  // unit -> (pair, stream, head): the heads that share a K/V range run next to
+  // one another, the units with the fewest keys last
   const int G = a.Hq / a.Hkv;
-  long long u = blockIdx.x;
-  const int h = (int)(u % a.Hq);
+  int u = blockIdx.x;
+  const int h = u % a.Hq;
   u /= a.Hq;
-  const int pair = n_pairs - 1 - (int)(u % n_pairs);
-  const int s = (int)(u / n_pairs);
+  const int s = u % a.S, pair = n_pairs - 1 - u / a.S;
   const int g = h / G;
   const int iA = pair * 256, iB = iA + 128;
   // key tiles: the sinks' [0, ns), then [fw, diagonal]
@@ -122,12 +152,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto key_tile = [&](int j) { return j < ns ? j : j - ns + fw; };
 
   auto bar_q = [&](int x) { return sb + L::kBar + 8u * x; };
+  constexpr int kS = L::kS, kSlots = L::kSlots;
   auto bar_full = [&](int sl) { return sb + L::kBar + 8u * (2 + sl); };
   auto bar_empty = [&](int sl) { return sb + L::kBar + 8u * (2 + kSlots + sl); };
-  auto bar_s = [&](int x) { return sb + L::kBar + 8u * (2 + 2 * kSlots + x); };
-  auto bar_p = [&](int x) { return sb + L::kBar + 8u * (4 + 2 * kSlots + x); };
-  auto bar_o = [&](int x) { return sb + L::kBar + 8u * (6 + 2 * kSlots + x); };
-  const uint32_t bar_done = sb + L::kBar + 8u * (8 + 2 * kSlots);
+  auto bar_s = [&](int b) { return sb + L::kBar + 8u * (2 + 2 * kSlots + b); };
+  auto bar_p = [&](int b, int half) { return sb + L::kBar + 8u * (2 + 2 * kSlots + kS + 2 * b + half); };
+  // P V of key tile j: phase j / 2 of its own parity's barrier.  Who sees S of
+  // tile j knows that P V of tile j - 3 is done, so j - 1 (the neighbour of j - 3
+  // on that barrier) can be waited for at any time
+  auto bar_pv = [&](int x, int j) { return sb + L::kBar + 8u * (2 + 2 * kSlots + 3 * kS + 2 * x + (j & 1)); };
+  const uint32_t bar_done = sb + L::kBar + 8u * (6 + 2 * kSlots + 3 * kS);
+  // K runs `lead` tiles ahead of V: the ring holds K_0 .. K_lead, V_0, K_lead+1, V_1, ...
+  const int lead = (kS - 1) / (nB > 0 ? 2 : 1);
+  auto pos_k = [&](int j) { return j <= lead ? j : 2 * j - lead; };
+  auto pos_v = [&](int j) { return min(n_load, lead + j + 1) + j; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmem);
   int* err = &g_err;
@@ -138,9 +176,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar_q(x), 1);
-      mbar_init(bar_s(x), 1);
-      mbar_init(bar_p(x), 4);
-      mbar_init(bar_o(x), 1);
+      mbar_init(bar_pv(x, 0), 1);
+      mbar_init(bar_pv(x, 1), 1);
+    }
+    for (int b = 0; b < kS; ++b) {
+      mbar_init(bar_s(b), 1);
+      mbar_init(bar_p(b, 0), 4);
+      mbar_init(bar_p(b, 1), 4);
     }
     for (int sl = 0; sl < kSlots; ++sl) {
       mbar_init(bar_full(sl), 1);
@@ -158,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // columns: S/P of A at 0, of B at 128, O of A at 256, O of B at 384
-  auto col_s = [](int x) { return (uint32_t)(x * 128); };
-  auto col_o = [](int x) { return (uint32_t)(256 + x * 128); };
+  // columns: kS buffers of S/P, then O of A, O of B
+  auto col_s = [](int b) { return (uint32_t)(b * 128); };
+  auto col_o = [](int x) { return (uint32_t)(kS * 128 + x * D); };
 
   if (warp < 4) regs_dec<kRegsLow>();
   if (warp == 0) {
@@ -174,14 +216,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_q(0);
       bool qb = false;
       int issued = 0;
+      int jk = 0, jv = 0;  // tiles of K and V so far
       for (int idx = 0; idx < 2 * n_load; ++idx) {
         const int sl = idx % kSlots;
+        const bool is_v = jk == n_load || (jk > lead + jv);
+        const int j = is_v ? jv++ : jk++;
         if (!mbar_wait(bar_empty(sl), ((idx / kSlots) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
-        const int r0 = key_tile(idx >> 1) * 128;
+        const int r0 = key_tile(j) * 128;
         mbar_arrive_expect_tx(bar_full(sl), L::kTile);
         const uint32_t dst = sb + L::kKV + sl * L::kTile;
         for (int at = 0; at < L::kAtoms; ++at)
-          tma_load_4d(dst + at * L::kAtomBytes, (idx & 1) ? &tm_v : &tm_k, bar_full(sl), at * 64, g, r0, s);
+          tma_load_4d(dst + at * L::kAtomBytes, is_v ? &tm_v : &tm_k, bar_full(sl), at * 64, g, r0, s);
         issued = idx + 1;
         if (idx == 0 && nB > 0) {
           load_q(1);
@@ -194,64 +239,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
       constexpr uint32_t id_o = idesc_bf16(128, D, false, true);
       const uint64_t dq0 = sdesc_sw128(sb + L::kQ, 16, 1024);
       const uint64_t dk0 = sdesc_sw128(sb + L::kKV, 16, 1024);
       const uint64_t dv0 = sdesc_sw128(sb + L::kKV, L::kAtomBytes, 1024);
-      auto slot16 = [&](int idx) { return (uint64_t)((idx % kSlots) * (L::kTile >> 4)); };
-      auto wait_slot = [&](int idx) {
-        return mbar_wait(bar_full(idx % kSlots), (idx / kSlots) & 1, err, kErrWaitLoad, abort_flag);
+      auto slot16 = [&](int pos) { return (uint64_t)((pos % kSlots) * (L::kTile >> 4)); };
+      auto wait_slot = [&](int pos) {
+        return warp_spin_wait(bar_full(pos % kSlots), (pos / kSlots) & 1, err, kErrWaitLoad, abort_flag);
       };
-      auto issue_s = [&](int x, int j) {  // S_x = Q_x K_j^T
-        const uint64_t dq = dq0 + (uint64_t)((x * L::kTile) >> 4), dk = dk0 + slot16(2 * j);
+      // query tile and key tile of S(q)
+      auto x_of = [&](int q) { return nB > 0 && (q >= 2 * nA || (q & 1)) ? 1 : 0; };
+      auto j_of = [&](int q) { return nB > 0 ? min(q >> 1, nA) : q; };
+      struct Next {  // S(q) = Q_x K_j^T
+        uint64_t dq, dk;
+        uint32_t s;
+      };
+      auto next_s = [&](int q) {
+        return Next{dq0 + (uint64_t)((x_of(q) * L::kTile) >> 4), dk0 + slot16(pos_k(j_of(q))), tmem + col_s(q % kS)};
+      };
+      auto issue_s = [&](Next n) {
+        asm volatile("" : "+l"(n.dq), "+l"(n.dk));  // the sums below stay here: hoisted, they would not fit the registers
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * L::kAtomBytes + (kk & 3) * 32) >> 4);
-          mma_ss(tmem + col_s(x), dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
+          mma_ss_e(n.s, n.dq + off, n.dk + off, id_s, kk > 0 ? 1u : 0u);
         }
-        mma_commit(bar_s(x));
       };
-      auto issue_pv = [&](int x, int j, int n) {  // O_x += P_x V_j
-        const uint64_t dv = dv0 + slot16(2 * j + 1);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + col_o(x), tmem + col_s(x) + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id_o,
-                 (j > 0 || kk > 0) ? 1u : 0u);
-        if (j == n - 1) mma_commit(bar_o(x));
+      auto commit_s = [&](int q) {
+        commit_e(bar_s(q % kS));
+        if (x_of(q) == 1 || nB == 0) commit_e(bar_empty(pos_k(j_of(q)) % kSlots));  // the last to read K_j
       };
-      bool ok = wait_slot(0) && mbar_wait(bar_q(0), 0, err, kErrWaitLoad, abort_flag);
-      if (ok) {
+      const int nq = nA + nB;
+      bool ok = true;
+      for (int q = 0; ok && q < min(kS, nq); ++q) {
+        if (!(ok = wait_slot(pos_k(j_of(q))) && warp_spin_wait(bar_q(x_of(q)), 0, err, kErrWaitLoad, abort_flag))) break;
         fence_after_sync();
-        issue_s(0, 0);
-        if (nB > 0 && (ok = mbar_wait(bar_q(1), 0, err, kErrWaitLoad, abort_flag))) {
-          fence_after_sync();
-          issue_s(1, 0);
-        }
-        if (ok) mma_commit(bar_empty(0));
+        issue_s(next_s(q));
+        commit_s(q);
       }
-      for (int j = 0; ok && j < n_load; ++j) {
-        if (!(ok = wait_slot(2 * j + 1))) break;  // V_j
-        const bool next_k = j + 1 < n_load;
-        if (j < nA) {
-          if (!(ok = mbar_wait(bar_p(0), j & 1, err, kErrWaitP, abort_flag))) break;
+      for (int q = 0; ok && q < nq; ++q) {
+        // all but P is waited for beforehand, tiles by their first reader only: the
+        // time from P to the next S is on the path that bounds the kernel
+        const int x = x_of(q), j = j_of(q), b = q % kS;
+        const bool more = q + kS < nq;
+        const Next n = next_s(more ? q + kS : q);
+        uint64_t dv = dv0 + slot16(pos_v(j));
+        const uint32_t o = tmem + col_o(x), p = tmem + col_s(b), turn = (q / kS) & 1;
+        asm volatile("" : "+l"(dv));
+        if ((x == 0 || j == nA) && !(ok = wait_slot(pos_v(j)))) break;
+        if (more && (x_of(q + kS) == 0 || j_of(q + kS) == nA) && !(ok = wait_slot(pos_k(j_of(q + kS))))) break;
+        // O_x += P V_j, each half of the keys once its P is there
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = warp_spin_wait(bar_p(b, half), turn, err, kErrWaitP, abort_flag))) break;
           fence_after_sync();
-          issue_pv(0, j, nA);
+#pragma unroll
+          for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            mma_ts_e(o, p + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
         }
-        if (next_k && !(ok = wait_slot(2 * (j + 1)))) break;  // K_{j+1}
-        if (j + 1 < nA) issue_s(0, j + 1);
-        if (j < nB) {
-          if (!(ok = mbar_wait(bar_p(1), j & 1, err, kErrWaitP, abort_flag))) break;
-          fence_after_sync();
-          issue_pv(1, j, nB);
+        if (!ok) break;
+        commit_e(bar_pv(x, j));  // before S's commit: who sees S(q + kS) may count on this one
+        if (more) {
+          issue_s(n);
+          commit_s(q + kS);
         }
-        mma_commit(bar_empty((2 * j + 1) % kSlots));
-        if (j + 1 < nB) issue_s(1, j + 1);
-        if (next_k) mma_commit(bar_empty((2 * (j + 1)) % kSlots));
+        if (x == 1 || nB == 0) commit_e(bar_empty(pos_v(j) % kSlots));
       }
-      mma_commit(bar_done);
-      drain_wait(bar_done, 0, err);
+      commit_e(bar_done);
+      if (lane == 0) drain_wait(bar_done, 0, err);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -260,27 +317,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const int i = iA + x * 128 + r;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t t_o = t_lane + col_o(x), t_s = t_lane + col_s(x);
+    const uint32_t t_o = t_lane + col_o(x);
     const float c = a.scale_log2;
     float m_used = -INFINITY, l = 0.f;
     bool ok = nX > 0;
     for (int j = 0; ok && j < nX; ++j) {
-      if (!(ok = warp_spin_wait(bar_s(x), j & 1, err, kErrWaitAcc, abort_flag))) break;
+      // place of this S tile in the sequence
+      const int q = nB == 0 ? j : x == 0 ? 2 * j : min(2 * j + 1, 2 * nA), b = q % kS;
+      const uint32_t t_s = t_lane + col_s(b);
+      if (!(ok = warp_spin_wait(bar_s(b), (q / kS) & 1, err, kErrWaitAcc, abort_flag))) break;
       fence_after_sync();
+      // A row sees columns below `end`, and from `lo` on or below `sink`.  Hidden
+      // ones become -inf in tensor memory before S is read: a separate rolled
+      // loop, so that the masks cost the main path no registers.  Per 32 columns
+      // the warp's rows (32 consecutive) tell whether there is anything to hide.
+      const int base = key_tile(j) * 128;
+      const int end0 = i - lane + 1 - base, lo0 = end0 - a.window, sink = a.n_sink - base;  // of lane 0
+      if (end0 < 128 || (lo0 + 31 > 0 && sink < 128)) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          if (end0 >= c0 + 32 && (lo0 + 31 <= c0 || sink >= c0 + 32)) continue;
+          // visible columns of the 32 as a mask (shifts of 64 bits: counts 0..32)
+          auto below = [&](int x) { return (uint32_t)((1ull << min(max(x - c0, 0), 32)) - 1); };
+          const uint32_t see = below(end0 + lane) & (~below(lo0 + lane) | below(sink));
+          uint32_t v[32];
+          tmem_ld32(t_s + c0, v);
+          tmem_ld_wait_dep(v);
+#pragma unroll
+          for (int jj = 0; jj < 32; ++jj)
+            if (!(see >> jj & 1)) v[jj] = __float_as_uint(-INFINITY);
+          tmem_st32(t_s + c0, v);
+        }
+        tmem_st_wait();
+      }
       uint32_t sv[128];
       tmem_ld32(t_s + 0, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
       tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
       tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
       tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
-      tmem_ld_wait();
-      // visible columns of this row: below `end`, and from `lo` on or below `sink`
-      const int base = key_tile(j) * 128;
-      const int end = i + 1 - base, lo = i - a.window + 1 - base, sink = a.n_sink - base;
-      if (__any_sync(0xffffffffu, end < 128 || (lo > 0 && sink < 128))) {
-#pragma unroll
-        for (int jj = 0; jj < 128; ++jj)
-          if (jj >= end || (jj < lo && jj >= sink)) sv[jj] = __float_as_uint(-INFINITY);
-      }
+      tmem_ld_wait_dep(*reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+      after_wait(*reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+      after_wait(*reinterpret_cast<uint32_t(*)[32]>(&sv[64]));
+      after_wait(*reinterpret_cast<uint32_t(*)[32]>(&sv[96]));
       float m8[8];
 #pragma unroll
       for (int q8 = 0; q8 < 8; ++q8) {
@@ -295,12 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool raise = m_new > m_used + kRaise;
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? ex2_approx(m_used - m_new) : 1.f;
-        if (j > 0) {  // O holds P V of every earlier tile: S_j was issued after them
+        if (j > 0) {
+          // O must hold P V of every earlier tile
+          if (!(ok = warp_wait(bar_pv(x, j - 1), ((j - 1) >> 1) & 1, err, kErrWaitAcc, abort_flag))) break;
+          fence_after_sync();
 #pragma unroll
           for (int c0 = 0; c0 < D / 32; ++c0) {
             uint32_t v[32];
             tmem_ld32(t_o + c0 * 32, v);
-            tmem_ld_wait();
+            tmem_ld_wait_dep(v);
 #pragma unroll
             for (int jj = 0; jj < 32; ++jj) v[jj] = __float_as_uint(__uint_as_float(v[jj]) * f);
             tmem_st32(t_o + c0 * 32, v);
@@ -325,14 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[jj] = pack_bf16x2(pp.x, pp.y);
         }
         tmem_st16(t_s + c0 * 16, pk);
+        if (c0 & 1) {  // the weights of 64 keys
+          tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p(b, c0 >> 1));
+        }
       }
-      tmem_st_wait();
       l += ls.x + ls.y;
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p(x));
     }
-    if (ok) ok = warp_wait(bar_o(x), 0, err, kErrWaitAcc, abort_flag);
+    if (ok) ok = warp_wait(bar_pv(x, nX - 1), ((nX - 1) >> 1) & 1, err, kErrWaitAcc, abort_flag);
     if (ok && !*abort_flag) {
       fence_after_sync();
       const float inv = 1.f / l;
@@ -342,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t v[32];
         tmem_ld32(t_o + c0 * 32, v);
-        tmem_ld_wait();
+        tmem_ld_wait_dep(v);
         uint32_t pk[16];
 #pragma unroll
         for (int jj = 0; jj < 16; ++jj) {
