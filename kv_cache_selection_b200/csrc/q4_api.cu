@@ -275,7 +275,10 @@ int sink_window_prefill(const void* q, const void* k, const void* v, int n_token
 
 int statekv_q4_status(int* code) {
   if (!code) return fail(STATEKV_ERR_INVALID_ARG, "null argument");
-  const cudaError_t e = skv::q4_attn_tc_status(code);
+  int tc = 0;
+  cudaError_t e = skv::q4_attn_status(code);
+  if (e == cudaSuccess) e = skv::q4_attn_tc_status(&tc);
+  if (*code == 0) *code = tc;
   if (e != cudaSuccess) return fail(STATEKV_ERR_CUDA, "status read failed: %s", cudaGetErrorString(e));
   return STATEKV_OK;
 }

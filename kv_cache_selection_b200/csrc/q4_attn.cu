@@ -4,8 +4,8 @@
 // With codes c, scales s and smallest values m per (token j, group g):
 //   q . k_j  = sum_g [ s_jg (q_g . c_jg) + m_jg sum(q_g) ],
 //   O        = sum_j p_j v_j = sum_j (p_j s_jg) (c_jg - 8) + sum_j p_j (m_jg + 8 s_jg).
-// The codes are exact fp16 numbers (one shift and one and-or give a pair of
-// 16 + c), so both sums are fp16 products with float32 accumulation, and the
+// The codes are exact fp16 numbers (an and-or gives a pair, with one rotation
+// for every four), so both sums are fp16 products with float32 accumulation, and the
 // scales meet float32 numbers only.  The rows are the G query heads of a KV
 // head times the text tokens, eight to a tile.
 //   Q: scaled by a power of two per row (largest element in [2^10, 2^11)); bf16
@@ -27,6 +27,7 @@
 // a worker writes one partial (max, sum, O) per (stream, KV head) it meets, and
 // q4_merge_kernel joins them in worker order with the text tokens' own part.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -43,13 +44,12 @@ constexpr float kRaise = 8.f;   // log2 headroom of the lazy row maximum
 constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
 constexpr float kPScale = 64.f; // P s <= 2^8 * 64 < 65504
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ int g_err;  // first error of the ring's waits of all calls on a device
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -65,17 +65,36 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ float2 unpack_half2(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
 
-// A pair of codes as fp16: 16 + c, or c - 8.
-template <int F>
-__device__ __forceinline__ uint32_t code_raw(uint32_t x) {
-  return q4_field<F>(x) | 0x4C004C00u;
+// The four fields of a word as fp16 pairs: c + 16, or c - 8.
+template <bool kCentred>
+__device__ __forceinline__ void codes_of(uint32_t x, uint32_t (&f)[4]) {
+  const uint32_t y = q4_turn(x);
+  f[0] = q4_raw<0>(x);
+  f[1] = q4_raw<1>(y);
+  f[2] = q4_raw<2>(x);
+  f[3] = q4_raw<3>(y);
+  if (kCentred) {
+    f[0] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[0]), __float2half2_rn(24.f)));
+    f[3] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[3]), __float2half2_rn(24.f)));
+  }
+  const __half2 off = __float2half2_rn(kCentred ? 264.f : 240.f);
+  f[1] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[1]), off));
+  f[2] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[2]), off));
 }
-template <int F>
-__device__ __forceinline__ uint32_t code_centred(uint32_t x) {
-  const uint32_t r = code_raw<F>(x);
-  return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&r), __half2half2(__ushort_as_half(0x4E00))));  // 24
+
+__device__ __forceinline__ void load_channels(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load_channels(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
 // The numbering of the visible blocks: of (s, g), first block and count; and
@@ -115,6 +134,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   const int row0 = blockIdx.y * kRows;
   uint8_t* ring = smem + warp * (kStages * B::kBytes);
   const uint32_t ring_u32 = tc::smem_u32(ring);
+  __shared__ __align__(8) uint64_t s_bars[kWarps * kStages];
+  __shared__ int s_abort;
+  volatile int* abort_flag = &s_abort;
+  const uint32_t bars = tc::smem_u32(s_bars + warp * kStages);
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    for (int i = 0; i < kWarps * kStages; ++i) tc::mbar_init(tc::smem_u32(s_bars + i), 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  int done = 0;     // blocks this warp has taken from its ring
+  bool ok = true;
 
   pdl_wait();
   pdl_trigger();
@@ -138,19 +169,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
     const int v1 = (int)min((long long)vis.count(), v0 + (x_end - x));
     const uint8_t* base = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
 
-    auto issue = [&](int v, int stage) {
-      if (v < v1) {
-        const uint8_t* src = base + (long long)vis.block(v) * B::kBytes;
-        const uint32_t dst = ring_u32 + stage * B::kBytes;
-#pragma unroll
-        for (int c = 0; c < (B::kBytes / 16 + 31) / 32; ++c)
-          if ((c + 1) * 32 <= B::kBytes / 16 || c * 32 + lane < B::kBytes / 16)
-            cp16(dst + (c * 32 + lane) * 16, src + (c * 32 + lane) * 16);
-      }
-      cp_commit();
+    // the warp's blocks v0 + warp, + kWarps, ...: its n-th (of the kernel) goes to
+    // stage n % kStages
+    auto issue = [&](int v, int n) {
+      const uint32_t bar = bars + 8u * (n % kStages);
+      tc::mbar_arrive_expect_tx(bar, B::kBytes);
+      bulk_load(ring_u32 + (n % kStages) * B::kBytes, base + (long long)vis.block(v) * B::kBytes, B::kBytes, bar);
     };
-#pragma unroll
-    for (int st = 0; st < kStages; ++st) issue(v0 + warp + st * kWarps, st);
+    int issued = done;
+    if (lane == 0)
+      for (int v = v0 + warp; v < v1 && issued < done + kStages; v += kWarps) issue(v, issued++);
+    issued = done + min(kStages, max(0, (v1 - v0 - warp + kWarps - 1) / kWarps));
 
     // ---- Q fragments, per-row scale and group sums
     uint32_t qf[NT][NS][MT][2];
@@ -167,9 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       if (r < R) {
         const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + r / G) * a.Hq + g * G + r % G) * D;
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) qv[w][e] = to_f(q[(w >> 1) * 64 + tig * 16 + (w & 1) * 8 + e]);
+        for (int w = 0; w < KW; ++w) load_channels(q + (w >> 1) * 64 + tig * 16 + (w & 1) * 8, qv[w]);
       }
       float top = 0.f;
 #pragma unroll
@@ -217,7 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       }
     }
 
-    float o[NT][MT][4], corr[NT][NG][2], l[NT][2], m[NT][2], vR[NG];
+    float o[NT][MT][4], corr[NT][NG][2], l[NT][2], m[NT][2], vR[NG], vs[NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -233,12 +260,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       }
     }
 #pragma unroll
-    for (int gg = 0; gg < NG; ++gg) vR[gg] = kMinR;
+    for (int gg = 0; gg < NG; ++gg) {
+      vR[gg] = kMinR;
+      vs[gg] = kPScale / kMinR;
+    }
 
-    int stage = 0;
-    for (int v = v0 + warp; v < v1; v += kWarps) {
-      cp_wait<kStages - 1>();
-      __syncwarp();
+    for (int v = v0 + warp; ok && v < v1; v += kWarps, ++done) {
+      const int stage = done % kStages;
+      if (!(ok = tc::warp_wait(bars + 8u * stage, (done / kStages) & 1, &g_err, tc::kErrWaitLoad, abort_flag))) break;
       const uint8_t* blk = ring + stage * B::kBytes;
       const int t0 = vis.block(v) * kQ4Tokens;
       bool full = t0 + kQ4Tokens <= vis.L;
@@ -266,24 +295,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             for (int e = 0; e < 4; ++e) acc[nt][gg][e] = 0.f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          uint32_t f[8];
-          if (NS == 2) {
-            f[0] = code_centred<0>(ka[w]), f[1] = code_centred<0>(kb[w]);
-            f[2] = code_centred<1>(ka[w]), f[3] = code_centred<1>(kb[w]);
-            f[4] = code_centred<2>(ka[w]), f[5] = code_centred<2>(kb[w]);
-            f[6] = code_centred<3>(ka[w]), f[7] = code_centred<3>(kb[w]);
-          } else {
-            f[0] = code_raw<0>(ka[w]), f[1] = code_raw<0>(kb[w]);
-            f[2] = code_raw<1>(ka[w]), f[3] = code_raw<1>(kb[w]);
-            f[4] = code_raw<2>(ka[w]), f[5] = code_raw<2>(kb[w]);
-            f[6] = code_raw<3>(ka[w]), f[7] = code_raw<3>(kb[w]);
-          }
+          uint32_t fa[4], fb[4];
+          codes_of<NS == 2>(ka[w], fa);
+          codes_of<NS == 2>(kb[w], fb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int ns = 0; ns < NS; ++ns) {
-              mma16816(acc[nt][w >> 1], f[0], f[1], f[2], f[3], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
-              mma16816(acc[nt][w >> 1], f[4], f[5], f[6], f[7], qf[nt][ns][2 * w + 1][0], qf[nt][ns][2 * w + 1][1]);
+              mma16816(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
+              mma16816(acc[nt][w >> 1], fa[2], fb[2], fa[3], fb[3], qf[nt][ns][2 * w + 1][0], qf[nt][ns][2 * w + 1][1]);
             }
         }
         const uint32_t* ks = reinterpret_cast<const uint32_t*>(blk + B::kKs) + (kt * 16 + gid) * NG;
@@ -297,8 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float part = fmaf(sc, acc[nt][gg][hh * 2 + e], mid * qsum[nt][gg][e]);
-                t[nt][kt][hh * 2 + e] = gg == 0 ? part : t[nt][kt][hh * 2 + e] + part;
+                const float sum = gg == 0 ? mid * qsum[nt][0][e] : fmaf(mid, qsum[nt][gg][e], t[nt][kt][hh * 2 + e]);
+                t[nt][kt][hh * 2 + e] = fmaf(sc, acc[nt][gg][hh * 2 + e], sum);
               }
           }
       }
@@ -316,9 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             mv[kt][hh][gg] = fmaf(sv[kt][hh][gg], 8.f, q4_min(sm));
           }
       // ---- masks: hidden tokens get a logit of -inf; a V scale no row uses gets 0
-      uint32_t seen = 0xffffffffu;  // bit nt*8 + kt*4 + hh*2 + e
       if (!full) {
-        seen = 0;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -335,8 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const bool ok = in && (keep || (long long)tok > (long long)vis.L + irow[nt][e] - a.window);
-                if (ok) seen |= 1u << (nt * 8 + kt * 4 + hh * 2 + e);
-                else t[nt][kt][hh * 2 + e] = -INFINITY;
+                if (!ok) t[nt][kt][hh * 2 + e] = -INFINITY;
               }
           }
       }
@@ -381,6 +398,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
           const float nr = fmaxf(vR[gg], up);
           fv[gg] = vR[gg] / nr;
           vR[gg] = nr;
+          vs[gg] = kPScale / nr;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -391,39 +409,50 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       }
       // ---- P, its sums, and P s as fp16 fragments
       uint32_t pf[NT][NS][NG][2][2];
-      float vs[NG];
+      auto weights = [&](auto careful) {
 #pragma unroll
-      for (int gg = 0; gg < NG; ++gg) vs[gg] = kPScale / vR[gg];
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const float p0 = tc::ex2_approx(t[nt][kt][hh * 2] - m0), p1 = tc::ex2_approx(t[nt][kt][hh * 2 + 1] - m1);
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+#pragma unroll
+              for (int gg = 0; gg < NG; ++gg) {
+                float s0 = sv[kt][hh][gg] * vs[gg], s1 = s0, m0v = mv[kt][hh][gg], m1v = m0v;
+                if (careful) {  // (the same roundings with and without)
+                  if (t[nt][kt][hh * 2] == -INFINITY) s0 = m0v = 0.f;
+                  if (t[nt][kt][hh * 2 + 1] == -INFINITY) s1 = m1v = 0.f;
+                }
+                const float x0 = p0 * s0, x1 = p1 * s1;
+                corr[nt][gg][0] = fmaf(p0, m0v, corr[nt][gg][0]);
+                corr[nt][gg][1] = fmaf(p1, m1v, corr[nt][gg][1]);
+                const __half2 hi = __floats2half2_rn(x0, x1);
+                pf[nt][0][gg][kt][hh] = transpose8x8(half2_bits(hi));
+                if (NS == 2) {
+                  const float2 h = __half22float2(hi);
+                  pf[nt][NS - 1][gg][kt][hh] = transpose8x8(half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y)));
+                }
+              }
+            }
+        }
+      };
+      // a NaN scale of a token that only some rows see stays out of the others
+      bool odd = false;
+      if (!full) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const float p0 = tc::ex2_approx(t[nt][kt][hh * 2] - m0), p1 = tc::ex2_approx(t[nt][kt][hh * 2 + 1] - m1);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            const bool ok0 = seen >> (nt * 8 + kt * 4 + hh * 2) & 1, ok1 = seen >> (nt * 8 + kt * 4 + hh * 2 + 1) & 1;
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-            for (int gg = 0; gg < NG; ++gg) {
-              const float sc = sv[kt][hh][gg] * vs[gg];
-              float x0 = p0 * sc, x1 = p1 * sc, y0 = p0 * mv[kt][hh][gg], y1 = p1 * mv[kt][hh][gg];
-              if (!full) {  // a hidden token's scale may be NaN
-                if (!ok0) x0 = y0 = 0.f;
-                if (!ok1) x1 = y1 = 0.f;
-              }
-              corr[nt][gg][0] += y0;
-              corr[nt][gg][1] += y1;
-              const __half2 hi = __floats2half2_rn(x0, x1);
-              pf[nt][0][gg][kt][hh] = transpose8x8(half2_bits(hi));
-              if (NS == 2) {
-                const float2 h = __half22float2(hi);
-                pf[nt][NS - 1][gg][kt][hh] = transpose8x8(half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y)));
-              }
-            }
-          }
+            for (int gg = 0; gg < NG; ++gg) odd |= mv[kt][hh][gg] != mv[kt][hh][gg];
+        odd = __any_sync(0xffffffffu, odd);
       }
+      if (odd) weights(std::true_type());
+      else weights(std::false_type());
       // ---- O^T += V^T P^T, 32 channels at a time
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -432,23 +461,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t x0 = half ? w.z : w.x, x1 = half ? w.w : w.y;
-          uint32_t f[8];
-          f[0] = code_centred<0>(x0), f[1] = code_centred<0>(x1), f[2] = code_centred<1>(x0), f[3] = code_centred<1>(x1);
-          f[4] = code_centred<2>(x0), f[5] = code_centred<2>(x1), f[6] = code_centred<3>(x0), f[7] = code_centred<3>(x1);
+          uint32_t fa[4], fb[4];
+          codes_of<true>(x0, fa);
+          codes_of<true>(x1, fb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int ns = 0; ns < NS; ++ns) {
-              mma16816(o[nt][2 * c + half], f[0], f[1], f[2], f[3], pf[nt][ns][gg][0][0], pf[nt][ns][gg][0][1]);
-              mma16816(o[nt][2 * c + half], f[4], f[5], f[6], f[7], pf[nt][ns][gg][1][0], pf[nt][ns][gg][1][1]);
+              mma16816(o[nt][2 * c + half], fa[0], fb[0], fa[1], fb[1], pf[nt][ns][gg][0][0], pf[nt][ns][gg][0][1]);
+              mma16816(o[nt][2 * c + half], fa[2], fb[2], fa[3], fb[3], pf[nt][ns][gg][1][0], pf[nt][ns][gg][1][1]);
             }
         }
       }
       __syncwarp();
-      issue(v + kStages * kWarps, stage);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (v + kStages * kWarps < v1) {
+        if (lane == 0) issue(v + kStages * kWarps, done + kStages);
+        ++issued;
+      }
     }
-    cp_wait<0>();
+    if (!ok) {  // a copy did not arrive in time: wait for what is in flight before the ring is reused
+      if (lane == 0)
+        for (int n = max(done, issued - kStages); n < issued; ++n) tc::drain_wait(bars + 8u * (n % kStages), (n / kStages) & 1, &g_err);
+      __syncwarp();
+    }
+    done = issued;
 
     // ---- the warps' results into shared memory (over the drained ring)
     __syncthreads();
@@ -501,6 +537,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       *reinterpret_cast<float4*>(p.part_o + (part * kRows + r) * D + c * 4) = acc;
       if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (part * kRows + r) * 2) = make_float2(mx, ls);
     }
+    // the next segment's copies come over what was written here
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     x += v1 - v0;
   }
@@ -677,6 +715,14 @@ cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspac
   const cudaError_t e = launch_q4_attn_tc(p, d, st);
   if (e != cudaSuccess) return e;
   return d == 128 ? launch_merge<__nv_bfloat16, 128>(p, st) : launch_merge<__nv_bfloat16, 64>(p, st);
+}
+
+cudaError_t q4_attn_status(int* code) {
+  cudaError_t e = cudaDeviceSynchronize();
+  const int zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(code, g_err, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err, &zero, sizeof(int));
+  return e;
 }
 
 }  // namespace skv

@@ -103,16 +103,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 __device__ __forceinline__ uint32_t bits2(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return bits2(__floats2half2_rn(lo, hi)); }
-// field F of a word as (c - 8) s, and as (c - 8) s + mid, in fp16
+// field F of a word (or of the word turned: q4_raw) as c - 8, (c - 8) s and
+// (c - 8) s + mid, in fp16
 template <int F>
-__device__ __forceinline__ uint32_t dequant(uint32_t w, uint32_t s) {
-  const uint32_t r = q4_field<F>(w) | 0x4C004C00u;  // 16 + c
-  return bits2(__hmul2(__hsub2(half2_of(r), __half2half2(__ushort_as_half(0x4E00))), half2_of(s)));
+__device__ __forceinline__ __half2 centred(uint32_t x) {
+  return __hsub2(half2_of(q4_raw<F>(x)), __float2half2_rn(Q4Bias<F>::value + 8.f));
 }
 template <int F>
-__device__ __forceinline__ uint32_t dequant(uint32_t w, uint32_t s, uint32_t mid) {
-  const uint32_t r = q4_field<F>(w) | 0x4C004C00u;  // 16 + c
-  return bits2(__hfma2(__hsub2(half2_of(r), __half2half2(__ushort_as_half(0x4E00))), half2_of(s), half2_of(mid)));
+__device__ __forceinline__ uint32_t dequant(uint32_t x, uint32_t s) {
+  return bits2(__hmul2(centred<F>(x), half2_of(s)));
+}
+template <int F>
+__device__ __forceinline__ uint32_t dequant(uint32_t x, uint32_t s, uint32_t mid) {
+  return bits2(__hfma2(centred<F>(x), half2_of(s), half2_of(mid)));
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
 
@@ -546,9 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
 #pragma unroll
         for (int ww = 0; ww < D / 32; ++ww) {
           const int gg = ww >> 1;
+          const uint32_t turned = q4_turn(w[ww]);
           *reinterpret_cast<uint4*>(dst + gg * L::kAtom + (((tig * 2 + (ww & 1)) ^ (tid & 7)) << 4)) =
-              make_uint4(dequant<0>(w[ww], s2[gg]), dequant<1>(w[ww], s2[gg]), dequant<2>(w[ww], s2[gg]),
-                         dequant<3>(w[ww], s2[gg]));
+              make_uint4(dequant<0>(w[ww], s2[gg]), dequant<1>(turned, s2[gg]), dequant<2>(w[ww], s2[gg]),
+                         dequant<3>(turned, s2[gg]));
         }
       }
       fence_proxy_async();
@@ -597,10 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
         const uint4 t0 = x[0], t1 = x[1];
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t turned = q4_turn(ws[e]);
           *reinterpret_cast<uint4*>(dst + (c * 4 + e) * 1024) =
-              make_uint4(dequant<0>(ws[e], t0.x, t0.y), dequant<1>(ws[e], t0.z, t0.w), dequant<2>(ws[e], t1.x, t1.y),
-                         dequant<3>(ws[e], t1.z, t1.w));
+              make_uint4(dequant<0>(ws[e], t0.x, t0.y), dequant<1>(turned, t0.z, t0.w), dequant<2>(ws[e], t1.x, t1.y),
+                         dequant<3>(turned, t1.z, t1.w));
+        }
       }
       fence_proxy_async();
       __syncwarp();

@@ -347,9 +347,6 @@ __device__ __forceinline__ float low_value(uint32_t field, float s, float m) {
 __device__ __forceinline__ float high_value(uint32_t field, float s, float m) {
   return fmaf(__uint_as_float((field >> 3 & 0x00780000u) | 0x41800000u) - 16.f, s, m);
 }
-__device__ __forceinline__ uint32_t field_of(uint32_t x, int f) {
-  return f == 0 ? q4_field<0>(x) : f == 1 ? q4_field<1>(x) : f == 2 ? q4_field<2>(x) : q4_field<3>(x);
-}
 __device__ __forceinline__ void store_channels(__nv_bfloat16* dst, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(dst) = make_uint4(tc::pack_bf16x2(x[0], x[1]), tc::pack_bf16x2(x[2], x[3]),
                                               tc::pack_bf16x2(x[4], x[5]), tc::pack_bf16x2(x[6], x[7]));
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(D) q4_read_kernel(Q4IoArgs a) {
         const float sc = q4_scale(sm), m = q4_min(sm);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = hi ? high_value(field_of(x[e], f), sc, m) : low_value(field_of(x[e], f), sc, m);
+        for (int e = 0; e < 8; ++e) v[e] = hi ? high_value(q4_field(x[e], f), sc, m) : low_value(q4_field(x[e], f), sc, m);
         store_channels(static_cast<T*>(a.v_out) + (row0 + (long long)t * a.Hkv) * D + c8 * 8, v);
       }
   } else {
@@ -408,8 +405,8 @@ __global__ void __launch_bounds__(D) q4_read_kernel(Q4IoArgs a) {
       float v[8];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        v[q4_k_channel(f, 0)] = low_value(field_of(x, f), sc, m);
-        v[q4_k_channel(f, 1)] = high_value(field_of(x, f), sc, m);
+        v[q4_k_channel(f, 0)] = low_value(q4_field(x, f), sc, m);
+        v[q4_k_channel(f, 1)] = high_value(q4_field(x, f), sc, m);
       }
       store_channels(static_cast<T*>(a.k_out) + (row0 + (long long)t * a.Hkv) * D + c8 * 8, v);
     }

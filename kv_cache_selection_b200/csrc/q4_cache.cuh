@@ -26,11 +26,12 @@
 //      9 + 2 tig} and the same + 16; d = 8 j + gid sits in chunk j/4, lane
 //      4 gid + tig, word j%4.
 // Inside a word the eight codes are four pairs (field f: one code in the low
-// half, one in the high), placed so that one shift or rotation and one and-or
-// turn a pair into two fp16 numbers 16 + c (code at mantissa bits 6..9).  As
-// nibbles, rotated left by two bits, a word is
+// half, one in the high), placed so that an and-or turns a pair into two fp16
+// numbers: fields 0 and 2 of the word itself, 3 and 1 of the word rotated left
+// by eight bits; 16 + c for 0 and 3 (code at mantissa bits 6..9), 256 + c for 2
+// and 1 (bits 2..5).  As nibbles, rotated left by two bits, a word is
 //   n      0    1    2    3    4    5    6    7
-//   field  2 l  0 l  1 l  3 h  2 h  0 h  1 h  3 l      (l, h: low, high half)
+//   field  2 l  0 l  1 h  3 h  2 h  0 h  1 l  3 l      (l, h: low, high half)
 // K: nibble n is channel n of the word's eight.  V: field f holds the tokens
 // 16 (f/2) + 8 (f%2) + 2 tig (low) and the next (high).
 #pragma once
@@ -57,26 +58,33 @@ struct Q4Block {
 
 __host__ __device__ constexpr int q4_block_bytes(int d) { return 32 * d + 256 * (d / kQ4Group); }
 
-constexpr uint32_t kQ4Mask = 0x03C003C0u;
-
-// pairs (code 2f | code 2f+1 << 16), f = 0..3 -> word
+// pairs (low code | high code << 16) of fields 0..3 -> word
 __host__ __device__ __forceinline__ uint32_t q4_pack(uint32_t p0, uint32_t p1, uint32_t p2, uint32_t p3) {
-  const uint32_t r = p3 << 6;
-  return (p0 << 6) | (p1 << 10) | (p2 << 2) | ((r >> 8) | (r << 24));
+  const uint32_t r = (p3 << 6) | (p1 << 2);
+  return (p0 << 6) | (p2 << 2) | ((r >> 8) | (r << 24));
 }
-// field f of a word, each code at bits 6..9 of its half
+// Field f of a word as fp16 numbers kQ4Bias<f> + c.
+__device__ __forceinline__ uint32_t q4_turn(uint32_t x) { return __funnelshift_l(x, x, 8); }
 template <int F>
-__device__ __forceinline__ uint32_t q4_field(uint32_t x) {
-  if (F == 1) x >>= 4;
-  if (F == 2) x <<= 4;
-  if (F == 3) x = __funnelshift_l(x, x, 8);
-  return x & kQ4Mask;
+struct Q4Bias {
+  static constexpr float value = F == 0 || F == 3 ? 16.f : 256.f;
+};
+// x: the word (fields 0, 2) or the word turned (fields 1, 3)
+template <int F>
+__device__ __forceinline__ uint32_t q4_raw(uint32_t x) {
+  return F == 0 || F == 3 ? (x & 0x03C003C0u) | 0x4C004C00u : (x & 0x003C003Cu) | 0x5C005C00u;
+}
+// Field f of a word, each code at bits 6..9 of its half.
+__device__ __forceinline__ uint32_t q4_field(uint32_t x, int f) {
+  if (f & 1) x = q4_turn(x);
+  if (f == 1 || f == 2) x <<= 4;
+  return x & 0x03C003C0u;
 }
 // Field and half of nibble n, and the K channel of (field, half).
 __host__ __device__ __forceinline__ constexpr int q4_field_of(int n) { return 0x31023102 >> (4 * n) & 3; }
-__host__ __device__ __forceinline__ constexpr int q4_half_of(int n) { return 0x78 >> n & 1; }
+__host__ __device__ __forceinline__ constexpr int q4_half_of(int n) { return 0x3C >> n & 1; }
 __host__ __device__ __forceinline__ constexpr int q4_k_channel(int f, int half) {
-  return (half ? 0x3465 : 0x7021) >> (4 * f) & 7;
+  return (half ? 0x3425 : 0x7061) >> (4 * f) & 7;
 }
 // Eight nibbles -> word.
 __device__ __forceinline__ uint32_t q4_rotate(uint32_t nibbles) { return __funnelshift_l(nibbles, nibbles, 2); }
