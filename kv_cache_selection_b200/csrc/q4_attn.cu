@@ -97,25 +97,29 @@ __device__ __forceinline__ void load_channels(const float* p, float (&x)[8]) {
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// The numbering of the visible blocks: of (s, g), first block and count; and
-// the worker that owns a block.
+// The numbering of the visible blocks of all (stream, KV head) and their deal to
+// the workers: q blocks each, the first r one more (32-bit arithmetic: the host
+// checks that a cache has less than 2^31 blocks).
 struct Deal {
-  long long total;
-  int W;
-  __device__ __forceinline__ long long first(int w) const { return total * w / W; }
-  __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * W - 1) / total); }
+  int total, W, q, r;
+  __device__ __forceinline__ int first(int w) const { return w * q + min(w, r); }
+  __device__ __forceinline__ int owner(int x) const {
+    const int head = r * (q + 1);
+    return x < head ? x / (q + 1) : r + (x - head) / q;
+  }
 };
 __device__ __forceinline__ Deal deal_of(const WindowArgs& a, int W) {
   Deal d;
-  d.W = W;
   d.total = 0;
   if (a.lengths) {
     for (int s = 0; s < a.S; ++s) d.total += visible_of(a, s).count();
   } else {
-    d.total = (long long)a.S * visible_of(a, 0).count();
+    d.total = a.S * visible_of(a, 0).count();
   }
   d.total *= a.Hkv;
-  if (d.total < W) d.W = (int)d.total;  // every worker that counts owns a block
+  d.W = min(W, d.total);  // every worker that counts owns a block
+  d.q = d.W ? d.total / d.W : 0;
+  d.r = d.total - d.q * d.W;
   return d;
 }
 
@@ -134,16 +138,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   const int row0 = blockIdx.y * kRows;
   uint8_t* ring = smem + warp * (kStages * B::kBytes);
   const uint32_t ring_u32 = tc::smem_u32(ring);
+  // a warp's ring is its own: barriers and abort flag need no block-wide barrier
   __shared__ __align__(8) uint64_t s_bars[kWarps * kStages];
-  __shared__ int s_abort;
-  volatile int* abort_flag = &s_abort;
+  __shared__ int s_abort[kWarps];
+  volatile int* abort_flag = s_abort + warp;
   const uint32_t bars = tc::smem_u32(s_bars + warp * kStages);
-  if (threadIdx.x == 0) {
-    s_abort = 0;
-    for (int i = 0; i < kWarps * kStages; ++i) tc::mbar_init(tc::smem_u32(s_bars + i), 1);
+  if (lane == 0) {
+    *abort_flag = 0;
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(bars + 8u * i, 1);
     tc::fence_mbar_init();
   }
-  __syncthreads();
+  __syncwarp();
   int done = 0;     // blocks this warp has taken from its ring
   bool ok = true;
 
@@ -151,24 +157,39 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   pdl_trigger();
   const Deal deal = deal_of(a, p.W);
   if ((int)blockIdx.x >= deal.W) return;
-  long long x = deal.first(blockIdx.x);
-  const long long x_end = deal.first(blockIdx.x + 1);
-  int s = 0;
-  long long s_base = 0;
+  int x = deal.first(blockIdx.x);
+  const int x_end = deal.first(blockIdx.x + 1);
+  int s = 0, s_base = 0;
   Visible vis = visible_of(a, 0);
   // text tokens of the tile's rows (rows behind R take the last one)
   const int i_first = row0 / G, i_last = (min(row0 + kRows, R) - 1) / G;
 
   while (x < x_end) {
-    while (x >= s_base + (long long)a.Hkv * vis.count()) {
-      s_base += (long long)a.Hkv * vis.count();
+    while (x >= s_base + a.Hkv * vis.count()) {
+      s_base += a.Hkv * vis.count();
       vis = visible_of(a, ++s);
     }
-    const int g = (int)((x - s_base) / vis.count());
-    const int v0 = (int)((x - s_base) % vis.count());
-    const int v1 = (int)min((long long)vis.count(), v0 + (x_end - x));
+    const int g = (x - s_base) / vis.count(), v0 = (x - s_base) - g * vis.count();
+    const int v1 = min(vis.count(), v0 + (x_end - x));
     const uint8_t* base = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
 
+    // Q's loads go out before the ring's, which would be ahead of them in every
+    // queue of the memory system
+    float qv[NT][KW][8];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + gid;
+      const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + r / G) * a.Hq + g * G + r % G) * D;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        if (r < R) {
+          load_channels(q + (w >> 1) * 64 + tig * 16 + (w & 1) * 8, qv[nt][w]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qv[nt][w][e] = 0.f;
+        }
+      }
+    }
     // the warp's blocks v0 + warp, + kWarps, ...: its n-th (of the kernel) goes to
     // stage n % kStages
     auto issue = [&](int v, int n) {
@@ -187,22 +208,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
     int irow[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + gid;
-      float qv[KW][8];
-#pragma unroll
-      for (int w = 0; w < KW; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) qv[w][e] = 0.f;
-      if (r < R) {
-        const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + r / G) * a.Hq + g * G + r % G) * D;
-#pragma unroll
-        for (int w = 0; w < KW; ++w) load_channels(q + (w >> 1) * 64 + tig * 16 + (w & 1) * 8, qv[w]);
-      }
       float top = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(qv[w][e]));
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(qv[nt][w][e]));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // largest element into [2^10, 2^11); 1 for a zero row or one with an infinity
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const float x0 = qv[w][q4_k_channel(f, 0)] * up, x1 = qv[w][q4_k_channel(f, 1)] * up;
+          const float x0 = qv[nt][w][q4_k_channel(f, 0)] * up, x1 = qv[nt][w][q4_k_channel(f, 1)] * up;
           const __half2 hi = __floats2half2_rn(x0, x1);
           const float2 h = __half22float2(hi);
           qf[nt][0][2 * w + (f >> 1)][f & 1] = half2_bits(hi);
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
     if (t != t) l = t;  // a NaN logit makes the row NaN
     join(t, 1.f, v);
   }
-  pdl_wait();
+  // where the partials are
   int w0 = 0, w1 = -1, r = 0;
   long long part0 = 0;
   const int sg = s * a.Hkv + g;
@@ -600,20 +610,21 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
     w1 = p.W - 1;
   } else if (vis.count() > 0) {
     const Deal deal = deal_of(a, p.W);
-    long long base = 0;
+    int base = 0;
     if (a.lengths) {
       for (int s2 = 0; s2 < s; ++s2) base += visible_of(a, s2).count();
     } else {
-      base = (long long)s * vis.count();
+      base = s * vis.count();
     }
-    base = base * a.Hkv + (long long)g * vis.count();
+    base = base * a.Hkv + g * vis.count();
     w0 = deal.owner(base);
     w1 = deal.owner(base + vis.count() - 1);
     part0 = (long long)(row / p.rows) * (p.W + a.S * a.Hkv) + sg;
     r = row % p.rows;
   }
+  pdl_wait();
   {
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     for (int w = w0 + warp; w <= w1; w += kMergeWarps * kBatch) {
       float2 ml[kBatch];
       float v[kBatch][E];
