@@ -88,6 +88,16 @@ int statekv_create_batched(statekv_t* h, int n_streams, int Hq, int Hkv, int d, 
                            int B, int max_frames, int dtype, int mask_mode,
                            int select_mode);
 
+/* How a handle holds the detailed state D.  NATIVE (default): keys and values
+ * in the handle's element type.  Q4: in 4 bits a value, the cache that the
+ * statekv_q4_* calls below describe (4.5 bits with its scales): each step
+ * quantises the frame's keys and values into it, C_n still keeps the frame's
+ * own values, and statekv_decode attends to what D holds.  Call it before any
+ * layer is allocated.
+ * Errors: INVALID_ARG, UNSUPPORTED (a layer is allocated, D too large). */
+typedef enum { STATEKV_DETAILED_NATIVE = 0, STATEKV_DETAILED_Q4 = 1 } statekv_detailed;
+int statekv_set_detailed_format(statekv_t h, int format);
+
 /* Allocate the state of layers 0..n_layers-1 now (synchronous; device memory
  * zero-filled).  Call before capturing prefill calls in a CUDA graph. */
 int statekv_reserve_layers(statekv_t h, int n_layers);
@@ -145,7 +155,11 @@ int statekv_prefill_frame_host(statekv_t h, int layer, const void* q, const void
  *   out [S][n_text][Hq][d]   (device, dtype)
  *   lse [S][Hq][n_text]      float32 natural-log log-sum-exp (device) or NULL
  * Text token i sees D tokens [0, frames*T) of the layer and text tokens 0..i.
- * D is read, not modified.  bf16 runs on the tensor cores with the G query
+ * D is read, not modified.  Decodes of one handle share their scratch: order
+ * them on one stream.  With D in 4 bits the call is statekv_q4_decode over it
+ * without a window (errors its waits record show in statekv_q4_status; a
+ * capture that needs more scratch than the handle has is refused with
+ * UNSUPPORTED, so run one such decode before it).  Otherwise bf16 runs on the tensor cores with the G query
  * heads of a KV group stacked in one tile, so each D tile crosses HBM once
  * per KV head; float32 runs on the CUDA cores.  Split scratch is allocated on
  * the first call that needs more than before (synchronous), then reused.
@@ -168,9 +182,20 @@ int statekv_get_compressed(statekv_t h, int layer, const void** k, const void** 
  * kept for decoding):
  *   k,v [S][Hkv][max_frames*T][d] (dtype), tokens [0, len) valid, in arrival
  *   order; pos [S][max_frames*T] int32.  len = frames*T.
- * Valid until destroy.  Errors: INVALID_ARG. */
+ * Any output pointer may be NULL.  Valid until destroy.  Errors: INVALID_ARG,
+ * UNSUPPORTED (k or v of a D in 4 bits). */
 int statekv_get_detailed(statekv_t h, int layer, const void** k, const void** v,
                          const int32_t** pos, int* len);
+
+/* Borrow the detailed state D of a layer of a handle that holds it in 4 bits:
+ *   cache     for the statekv_q4_* calls, with the handle's n_streams, Hkv and
+ *             d and `capacity` = max_frames*T; tokens [0, len) valid, in
+ *             arrival order (to read them back, or to decode with a window);
+ *   pos [S][max_frames*T] int32; len = frames*T.
+ * Any output pointer may be NULL.  Valid until destroy.  Errors: INVALID_ARG,
+ * UNSUPPORTED (D is not in 4 bits). */
+int statekv_get_detailed_q4(statekv_t h, int layer, void** cache, int* capacity,
+                            const int32_t** pos, int* len);
 
 /* Borrow the per-row statistics of the most recent prefill_frame call (of
  * whichever layer it was):
@@ -388,7 +413,8 @@ int statekv_q4_status(int* code);
  * window >= 1, n_sink >= 0.  Work grows with n_tokens x (window + n_sink).  A
  * key or value the mask hides takes no part, whatever it holds (a bf16 row that
  * shares a tile of 128 keys with a hidden NaN or infinity is computed a second
- * time, slowly, and may differ in its last bits).  No memory is allocated.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * time, slowly, and may differ in its last bits).  No memory is allocated.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int sink_window_prefill(const void* q, const void* k, const void* v, int n_tokens, int Hq, int Hkv,
                         int d, int dtype, int window, int n_sink, void* out, float* lse,
                         void* stream);

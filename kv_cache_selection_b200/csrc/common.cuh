@@ -117,7 +117,7 @@ struct GatherArgs {
   const void* kf;  const void* vf;   // frame [s][t][g][d]
   void* kc_new;    void* vc_new;     // next C [s][g][B][d]
   const int32_t* idx;                // [s][g][B] kept pool indices (row 0 in global mode)
-  void* kd;        void* vd;         // D [s][g][max_tok][d]
+  void* kd;        void* vd;         // D [s][g][max_tok][d], or null: append the positions alone
   int32_t* pos_d;                    // [s][max_tok]
   const int32_t* pos_f;              // [s][T]
   const int32_t* pos_c;              // current C positions [s][g][B]

@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(256) gather_append_kernel(GatherArgs a, int n_
     const int per = is_c ? c_blocks : d_blocks;
     const int sg = t2 / per;                     // s * Hkv + g
     const int r0 = (t2 - sg * per) * R;
-    const int g = sg % a.Hkv, s = sg / a.Hkv;
+    const int heads = is_c || a.kd ? a.Hkv : 1;  // without kd a stream's positions are one row of tasks
+    const int g = sg % heads, s = sg / heads;
     const int n_rows = min(R, (is_c ? a.m_new : a.T) - r0);
     const int4* src[U];
     int4* dst[U];
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(256) gather_append_kernel(GatherArgs a, int n_
         const bool isv = w >= VPR;
         const int col = isv ? w - VPR : w;
         const int t = r0 + rl;
-        ok[u] = rl < n_rows;
+        ok[u] = rl < n_rows && a.kd != nullptr;
         src[u] = reinterpret_cast<const int4*>(static_cast<const char*>(isv ? a.vf : a.kf) +
                                                (((long long)s * a.T + t) * a.Hkv + g) * a.row_bytes) + col;
         dst[u] = reinterpret_cast<int4*>(static_cast<char*>(isv ? a.vd : a.kd) +
@@ -551,7 +552,7 @@ static cudaError_t launch_gather_vpr(const GatherArgs& a, int n_sm, cudaStream_t
   constexpr int R = GatherShape<VPR>::kR;
   const int per_c = (a.m_new + R - 1) / R, per_d = (a.T + R - 1) / R;
   const long long n_c = (long long)a.S * a.Hkv * per_c;
-  const long long n_tasks = n_c + (long long)a.S * a.Hkv * per_d;
+  const long long n_tasks = n_c + (long long)a.S * (a.kd ? a.Hkv : 1) * per_d;
   if (n_tasks == 0) return cudaSuccess;
   long long blocks = (n_tasks + 7) / 8;        // eight warps per block
   const long long cap = (long long)n_sm * 8;   // one resident wave

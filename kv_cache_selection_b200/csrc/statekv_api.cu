@@ -6,7 +6,8 @@
 //   (a) attention of the frame's queries over [C_{n-1}; frame]  -> out, lse
 //   (b) score pass: column mass of the normalised weights       -> partials
 //   (c) top-B select over the pool                              -> kept list
-//   (d) gather of the kept rows into the other C buffer + append to D
+//   (d) gather of the kept rows into the other C buffer + append to D (with D
+//       in 4 bits its keys and values follow in a launch of their own)
 // on the caller's stream with no host synchronisation.
 #include <cuda_runtime.h>
 
@@ -43,6 +44,7 @@ struct LayerState {
   float* scorec[2] = {nullptr, nullptr};
   void* kd = nullptr;
   void* vd = nullptr;
+  void* d4 = nullptr;  // D in 4 bits (STATEKV_DETAILED_Q4) instead of kd and vd
   int32_t* posd = nullptr;
   // per-step scratch of this layer (each layer has its own, so that steps of
   // different layers may run concurrently on different streams)
@@ -87,6 +89,11 @@ struct statekv_handle {
   float* dec_o = nullptr;
   float* dec_ml = nullptr;
   size_t dec_o_bytes = 0, dec_ml_bytes = 0;
+  int d_format = STATEKV_DETAILED_NATIVE;
+  // workspace of statekv_decode over D in 4 bits, grown on demand; the ones it
+  // outgrew stay until destroy, since captured graphs may hold them
+  void* dec_ws = nullptr;
+  long long dec_ws_bytes = 0;
   std::string err;
   std::vector<void*> allocs;
   // launch accounting and optional per-stage event timing
@@ -131,6 +138,18 @@ int dev_alloc(statekv_t h, void** p, size_t bytes) {
   return STATEKV_OK;
 }
 
+// dev_alloc without the zero fill.
+int raw_alloc(statekv_t h, void** p, size_t bytes) {
+  const cudaError_t e = cudaMalloc(p, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    *p = nullptr;
+    return set_err(h, STATEKV_ERR_OOM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
+  }
+  h->allocs.push_back(*p);
+  return STATEKV_OK;
+}
+
 int check_shape(statekv_t h, int S, int Hq, int Hkv, int d, int T, int B, int max_frames, int dtype,
                 int mask, int select) {
   if (S < 1 || Hq < 1 || Hkv < 1 || T < 1 || B < 0 || max_frames < 1)
@@ -164,8 +183,14 @@ int alloc_layer(statekv_t h, LayerState& L) {
     if ((rc = dev_alloc(h, (void**)&L.posc[b], cint))) return rc;
     if ((rc = dev_alloc(h, (void**)&L.scorec[b], cint))) return rc;
   }
-  if ((rc = dev_alloc(h, &L.kd, dbytes))) return rc;
-  if ((rc = dev_alloc(h, &L.vd, dbytes))) return rc;
+  if (h->d_format == STATEKV_DETAILED_Q4) {
+    // no zero fill: what was not appended is never read
+    const long long b4 = statekv_q4_bytes(h->S, h->Hkv, h->d, (int)max_tok);
+    if ((rc = raw_alloc(h, &L.d4, (size_t)b4))) return rc;
+  } else {
+    if ((rc = dev_alloc(h, &L.kd, dbytes))) return rc;
+    if ((rc = dev_alloc(h, &L.vd, dbytes))) return rc;
+  }
   if ((rc = dev_alloc(h, (void**)&L.posd, (size_t)h->S * max_tok * 4))) return rc;
   const size_t S = h->S, pool = (size_t)h->B + h->T;
   if ((rc = dev_alloc(h, (void**)&L.lse, S * h->Hq * h->T * 4)) ||
@@ -399,6 +424,20 @@ int statekv_create(statekv_t* out, int Hq, int Hkv, int d, int T, int B, int max
   return statekv_create_batched(out, 1, Hq, Hkv, d, T, B, max_frames, dtype, mask_mode, select_mode);
 }
 
+int statekv_set_detailed_format(statekv_t h, int format) {
+  if (!h) return set_err(nullptr, STATEKV_ERR_INVALID_ARG, "null handle");
+  if (format != STATEKV_DETAILED_NATIVE && format != STATEKV_DETAILED_Q4)
+    return set_err(h, STATEKV_ERR_INVALID_ARG, "bad detailed format %d", format);
+  for (const LayerState& L : h->layers)
+    if (L.ready) return set_err(h, STATEKV_ERR_UNSUPPORTED, "the detailed format is set before the first layer is allocated");
+  if (format == STATEKV_DETAILED_Q4) {
+    const long long b4 = statekv_q4_bytes(h->S, h->Hkv, h->d, h->max_frames * h->T);
+    if (b4 < 0) return set_err(h, (int)b4, "%s", std::string(g_free_error).c_str());
+  }
+  h->d_format = format;
+  return STATEKV_OK;
+}
+
 int statekv_reserve_layers(statekv_t h, int n_layers) {
   if (!h) return set_err(nullptr, STATEKV_ERR_INVALID_ARG, "null handle");
   if (n_layers < 0) return set_err(h, STATEKV_ERR_INVALID_ARG, "negative layer count");
@@ -629,6 +668,21 @@ int prefill_step(statekv_t h, int layer, const void* q, const void* k, const voi
     sc.done();
   }
 
+  if (L->d4) {
+    skv::Q4IoArgs qa{};
+    qa.cache = L->d4;
+    qa.k = k;
+    qa.v = v;
+    qa.start = ga.d_len;
+    qa.n = T;
+    qa.S = S;
+    qa.Hkv = Hkv;
+    qa.capacity = ga.max_tok;
+    StageScope sc(h, st, STATEKV_STAGE_GATHER);
+    if ((e = skv::launch_q4_append(qa, h->dtype, d, st, true)) != cudaSuccess) return launch_err(h, e, "4-bit append");
+    sc.done();
+  }
+
   L->m = m_new;
   L->cur = nxt;
   L->frames += 1;
@@ -742,6 +796,30 @@ int statekv_decode(statekv_t h, int layer, const void* q, const void* k, const v
   const long long max_tok = (long long)h->max_frames * T;
   const float scale_log2 = skv::kLog2e / sqrtf((float)d);
   cudaError_t e;
+  if (L.d4) {
+    const long long need = statekv_q4_decode_workspace(S, Hq, Hkv, d, n_text, h->dtype);
+    if (need < 0) return set_err(h, (int)need, "%s", std::string(g_free_error).c_str());
+    if (need > h->dec_ws_bytes) {
+      cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+      if ((e = cudaStreamIsCapturing(st, &cap)) != cudaSuccess)
+        return set_err(h, STATEKV_ERR_CUDA, "stream query failed: %s", cudaGetErrorString(e));
+      if (cap != cudaStreamCaptureStatusNone)
+        return set_err(h, STATEKV_ERR_UNSUPPORTED, "a decode of %d text tokens needs %lld bytes of scratch: run one before the capture",
+                       n_text, need);
+      void* ws;
+      const int rc = raw_alloc(h, &ws, (size_t)need);
+      if (rc) return rc;
+      h->dec_ws = ws;
+      h->dec_ws_bytes = need;
+    }
+    StageScope sc(h, st, STATEKV_STAGE_DECODE);
+    const int rc = statekv_q4_decode(L.d4, S, Hq, Hkv, d, (int)max_tok, q, k, v, n_text, h->dtype, N, nullptr, 0, 0, out,
+                                     lse, h->dec_ws, need, stream);
+    sc.done();
+    if (rc) return set_err(h, rc, "%s", std::string(g_free_error).c_str());
+    ++h->launches;  // the merge
+    return STATEKV_OK;
+  }
   if (h->dtype != STATEKV_BF16) {
     skv::AttnArgs aa{};
     aa.q = q;
@@ -872,8 +950,23 @@ int statekv_get_detailed(statekv_t h, int layer, const void** k, const void** v,
   if (layer < 0 || (size_t)layer >= h->layers.size() || !h->layers[layer].ready)
     return set_err(h, STATEKV_ERR_INVALID_ARG, "unknown layer %d", layer);
   const LayerState& L = h->layers[layer];
+  if (L.d4 && (k || v))
+    return set_err(h, STATEKV_ERR_UNSUPPORTED, "D is held in 4 bits: statekv_get_detailed_q4 returns it");
   if (k) *k = L.kd;
   if (v) *v = L.vd;
+  if (pos) *pos = L.posd;
+  if (len) *len = L.frames * h->T;
+  return STATEKV_OK;
+}
+
+int statekv_get_detailed_q4(statekv_t h, int layer, void** cache, int* capacity, const int32_t** pos, int* len) {
+  if (!h) return set_err(nullptr, STATEKV_ERR_INVALID_ARG, "null handle");
+  if (layer < 0 || (size_t)layer >= h->layers.size() || !h->layers[layer].ready)
+    return set_err(h, STATEKV_ERR_INVALID_ARG, "unknown layer %d", layer);
+  const LayerState& L = h->layers[layer];
+  if (!L.d4) return set_err(h, STATEKV_ERR_UNSUPPORTED, "D is held in its own type: statekv_get_detailed returns it");
+  if (cache) *cache = L.d4;
+  if (capacity) *capacity = h->max_frames * h->T;
   if (pos) *pos = L.posd;
   if (len) *len = L.frames * h->T;
   return STATEKV_OK;

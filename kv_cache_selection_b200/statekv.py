@@ -22,6 +22,7 @@ LIB_PATH = os.environ.get("STATEKV_LIB", os.path.join(_PKG, "lib", "libstatekv.s
 BF16, F32 = 0, 1
 MASKS = {"frame_causal": 0, "frame_bidir": 1}
 SELECTS = {"global": 0, "per_kv_head": 1, "recency": 2}
+DETAILED = {"native": 0, "q4": 1}
 N_STAGES = 8
 STAGES = ["attention", "attention_combine", "score", "select", "gather", "decode", "decode_combine",
           "attention_chained"]
@@ -47,6 +48,8 @@ _SIGS = {
     "statekv_prefill_frame_host": (_i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "statekv_get_compressed": (_i, [_vp, _i, _pp, _pp, _pp, _pp, _ip]),
     "statekv_get_detailed": (_i, [_vp, _i, _pp, _pp, _pp, _ip]),
+    "statekv_set_detailed_format": (_i, [_vp, _i]),
+    "statekv_get_detailed_q4": (_i, [_vp, _i, _pp, _ip, _pp, _ip]),
     "statekv_get_step_stats": (_i, [_vp, _pp, _pp, _ip]),
     "statekv_frames": (_i, [_vp, _i]),
     "statekv_profile_enable": (_i, [_vp, _i]),
@@ -128,7 +131,7 @@ def borrow(ptr: int, shape, dtype: torch.dtype) -> torch.Tensor:
     if dtype == torch.bfloat16:
         t = torch.as_tensor(_DevView(ptr, shape, "<i2"), device="cuda")
         return t.view(torch.bfloat16)
-    typestr = {torch.float32: "<f4", torch.int32: "<i4"}[dtype]
+    typestr = {torch.float32: "<f4", torch.int32: "<i4", torch.uint8: "|u1"}[dtype]
     return torch.as_tensor(_DevView(ptr, shape, typestr), device="cuda")
 
 
@@ -146,15 +149,21 @@ def _need(t: torch.Tensor, shape, dtype, name):
 
 
 class StateKV:
-    """One StateKV cache builder (one or n_streams video streams, any layers)."""
+    """One StateKV cache builder (one or n_streams video streams, any layers).
+
+    detailed="q4" holds the detailed state D in 4 bits a value (Q4Cache):
+    get_detailed and decode then deal with what that keeps of the keys and values.
+    """
 
     def __init__(self, Hq, Hkv, d, T, B, max_frames, dtype="bf16", mask="frame_causal",
-                 select="global", n_streams=1):
+                 select="global", n_streams=1, detailed="native"):
+        if detailed not in DETAILED:
+            raise ValueError(f"detailed must be one of {sorted(DETAILED)}, not {detailed!r}")
         self.Hq, self.Hkv, self.d, self.T, self.B = Hq, Hkv, d, T, B
         self.max_frames, self.S = max_frames, n_streams
         self.dtype_code = _dtype_code(dtype)
         self.dtype = _torch_dtype(self.dtype_code)
-        self.mask, self.select = mask, select
+        self.mask, self.select, self.detailed = mask, select, detailed
         lead = () if n_streams == 1 else (n_streams,)
         self._step_shapes = (lead + (T, Hq, d), lead + (T, Hkv, d), lead + (T,))  # q/out, k/v, pos
         h = ctypes.c_void_p()
@@ -162,6 +171,8 @@ class StateKV:
                                         self.dtype_code, MASKS[mask], SELECTS[select])
         _check(rc)
         self._h = h
+        if detailed != "native":
+            _check(lib.statekv_set_detailed_format(h, DETAILED[detailed]), h)
 
     @property
     def handle(self):
@@ -268,7 +279,10 @@ class StateKV:
             len=n.value)
 
     def get_detailed(self, layer):
-        """Borrowed views of D: k, v [S][Hkv][max_frames*T][d], pos [S][max_frames*T], len."""
+        """Borrowed views of D: k, v [S][Hkv][max_frames*T][d], pos [S][max_frames*T], len;
+        with detailed="q4" a Q4Cache `cache` over it instead of k and v."""
+        if self.detailed == "q4":
+            return self._detailed_q4(layer)
         k, v, p = (ctypes.c_void_p() for _ in range(3))
         n = ctypes.c_int()
         _check(lib.statekv_get_detailed(self._h, layer, ctypes.byref(k), ctypes.byref(v),
@@ -276,6 +290,15 @@ class StateKV:
         S, H, N, d = self.S, self.Hkv, self.max_frames * self.T, self.d
         return dict(k=borrow(k.value, (S, H, N, d), self.dtype), v=borrow(v.value, (S, H, N, d), self.dtype),
                     pos=borrow(p.value, (S, N), torch.int32), len=n.value)
+
+    def _detailed_q4(self, layer):
+        c, p = ctypes.c_void_p(), ctypes.c_void_p()
+        cap, n = ctypes.c_int(), ctypes.c_int()
+        _check(lib.statekv_get_detailed_q4(self._h, layer, ctypes.byref(c), ctypes.byref(cap), ctypes.byref(p),
+                                           ctypes.byref(n)), self._h)
+        data = borrow(c.value, (lib.statekv_q4_bytes(self.S, self.Hkv, self.d, cap.value),), torch.uint8)
+        return dict(cache=Q4Cache(self.Hkv, self.d, cap.value, self.S, data=data),
+                    pos=borrow(p.value, (self.S, cap.value), torch.int32), len=n.value)
 
     def step_stats(self):
         """Borrowed views of the last step's lse [S][Hq][T] and pool scores [S][Hkv][B+T]."""
@@ -361,17 +384,21 @@ class Q4Cache:
 
     A group of 64 channels of a token's key or value keeps codes 0..15, a scale
     and a smallest value (include/statekv.h has the rounding).  The buffer is a
-    torch tensor, `data`, that this object owns; every call runs on `stream`, or
-    on the current stream.  Leading [S] dimensions of q, k and v may be left out
+    torch tensor, `data` (a new one, unless one is given); every call runs on
+    `stream`, or on the current stream.  Leading [S] dimensions of q, k and v may be left out
     when n_streams is 1.
     """
 
-    def __init__(self, Hkv, d, capacity, n_streams=1, device=None):
+    def __init__(self, Hkv, d, capacity, n_streams=1, device=None, data=None):
         n = lib.statekv_q4_bytes(n_streams, Hkv, d, capacity)
         if n < 0:
             _check(int(n))
         self.Hkv, self.d, self.capacity, self.S = Hkv, d, capacity, n_streams
-        self.data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+        if data is None:
+            data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+        else:
+            _need(data, (n,), torch.uint8, "data")
+        self.data = data
         self._dev = self.data.get_device()
         self._ptr = self.data.data_ptr()
         self._proto = {t: torch.empty((), dtype=t, device=self.data.device) for t in (torch.bfloat16, torch.float32)}

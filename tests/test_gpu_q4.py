@@ -564,3 +564,133 @@ def test_prefill_then_generate_over_the_cache():
         k, v = torch.cat([k, nk], 1), torch.cat([v, nv], 1)
     for t, x in zip(c.read(0, n + 3), (k, v)):
         assert same(t.cpu(), exact_tensor(O.q4_held(x), dtype))
+
+
+# ------------------------------------------------- a handle's detailed state D
+def handles(S, T, frames, dtype, Hq=6, Hkv=2, d=64, B=40):
+    skv = _skv()
+    return [skv.StateKV(Hq, Hkv, d, T, B, frames + 1, dtype=dtype, n_streams=S, detailed=x) for x in ("native", "q4")]
+
+
+def frame(seed, S, T, Hq, Hkv, d, dtype):
+    k, v = tokens(seed, S, T, Hkv, d, dtype)
+    q, _ = tokens(seed + 500, S, T, Hq, d, dtype, loud=False)
+    pos = (torch.arange(T, dtype=torch.int32) + seed * T).expand(S, T).contiguous()
+    return [t if S > 1 else t[0] for t in (q, k, v, pos)]
+
+
+@cuda
+@pytest.mark.parametrize("host", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S,T", [(1, 37), (2, 64), (1, 1)])
+def test_handle_with_detailed_state_in_4_bits(S, T, dtype, host):
+    """Frames of 37, 64 and 1 tokens: every result of a step is the native
+    handle's, bit for bit; D holds the rounded keys and values; a decode attends
+    to them (with the 8-row and, in bf16, the 128-row kernel)."""
+    Hq, Hkv, d, frames = 6, 2, 64, 3
+    hs = handles(S, T, frames, dtype)
+    seen = []
+    for n in range(frames):
+        ins = frame(n, S, T, Hq, Hkv, d, dtype)
+        seen.append(ins)
+        outs = []
+        for h in hs:
+            if host and n != 1:          # the second frame comes from device buffers
+                pinned = [t.pin_memory() for t in ins]
+                out = torch.empty_like(pinned[0]).pin_memory()
+                h.prefill_frame_host(0, *pinned, out)
+                torch.cuda.synchronize()
+            else:
+                out = h.prefill_frame(0, *(t.cuda() for t in ins)).cpu()
+            outs.append(out)
+        assert same(*outs)
+        stats = [h.step_stats() for h in hs]
+        assert same(stats[0]["lse"], stats[1]["lse"])
+        C = [h.get_compressed(0) for h in hs]
+        m = C[0]["len"]
+        assert m == C[1]["len"]
+        for key in ("k", "v", "pos", "score"):
+            assert same(C[0][key][:, :, :m], C[1][key][:, :, :m]), key
+    D0, D1 = (h.get_detailed(0) for h in hs)
+    N = frames * T
+    assert D0["len"] == D1["len"] == N and same(D0["pos"][:, :N], D1["pos"][:, :N])
+    k, v = (torch.cat([(f[i] if S > 1 else f[i][None]) for f in seen], 1) for i in (1, 2))
+    for got, x in zip(D1["cache"].read(0, N, dtype=dtype), (k, v)):
+        assert same(got.cpu(), exact_tensor(O.q4_held(x), dtype))
+    for n in (1, 9):
+        nk, nv = tokens(70 + n, S, n, Hkv, d, dtype)
+        nq, _ = tokens(80 + n, S, n, Hq, d, dtype, loud=False)
+        ins = [t.cuda() if S > 1 else t[0].cuda() for t in (nq, nk, nv)]
+        out, lse = hs[1].decode(0, *ins)
+        again, _ = D1["cache"].decode(*ins, N)
+        assert same(out, again)
+        part, plse = D1["cache"].decode(*ins, N, window=20, n_sink=3)   # the borrowed cache, with a window
+        for o, z, window, n_sink in ((out, lse, 0, 0), (part, plse, 20, 3)):
+            for s in range(S):
+                want = reference(nq[s], nk[s], nv[s], O.q4_held(k[s]), O.q4_held(v[s]), window, n_sink)
+                check_attention(o[s] if S > 1 else o, z[s] if S > 1 else z, want, dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
+    assert hs[1].device_status() == 0 and _skv().q4_status() == 0
+    for h in hs:
+        h.close()
+
+
+@cuda
+def test_handle_decode_before_any_frame_and_format_refusals():
+    skv = _skv()
+    native, q4 = handles(1, 16, 2, "bf16")
+    for h in (native, q4):
+        h.reserve_layers(1)
+    q, k, v, _ = (t.cuda() for t in frame(1, 1, 16, 6, 2, 64, "bf16"))
+    a, b = (h.decode(0, q[:2].contiguous(), k[:2].contiguous(), v[:2].contiguous()) for h in (native, q4))
+    assert q4.get_detailed(0)["len"] == 0
+    want = reference(q[:2].cpu(), k[:2].cpu(), v[:2].cpu(), None, None, 0, 0)
+    check_attention(b[0], b[1], want, "bf16", 2.0 ** -11)
+    check_attention(a[0], a[1], want, "bf16", 2.0 ** -8)
+    lib = skv.lib
+    for h, fmt in ((native, 1), (q4, 0)):
+        assert lib.statekv_set_detailed_format(h.handle, fmt) == -2     # a layer is there
+        assert lib.statekv_set_detailed_format(h.handle, 7) == -1
+    import ctypes
+    p = ctypes.c_void_p()
+    assert lib.statekv_get_detailed(q4.handle, 0, ctypes.byref(p), None, None, None) == -2
+    assert lib.statekv_get_detailed(q4.handle, 0, None, None, ctypes.byref(p), None) == 0 and p.value
+    assert lib.statekv_get_detailed_q4(native.handle, 0, ctypes.byref(p), None, None, None) == -2
+    assert lib.statekv_get_detailed_q4(q4.handle, 3, None, None, None, None) == -1
+    for h in (native, q4):
+        h.close()
+
+
+@cuda
+def test_handle_decode_captured_in_a_graph():
+    """A captured decode reads the handle's D and scratch; one that needs more
+    scratch than there is is refused, and later growth leaves the graph's alone."""
+    S, T, Hq, Hkv, d = 1, 50, 6, 2, 64
+    skv = _skv()
+    h = handles(S, T, 3, "bf16")[1]
+    for n in range(3):
+        h.prefill_frame(0, *(t.cuda() for t in frame(n, S, T, Hq, Hkv, d, "bf16")))
+    q, k, v, _ = (t.cuda() for t in frame(9, S, T, Hq, Hkv, d, "bf16"))
+    one = [t[:1].clone() for t in (q, k, v)]
+    many = [t.contiguous() for t in (q, k, v)]
+    want = h.decode(0, *one)[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            out, _ = h.decode(0, *one)
+            with pytest.raises(skv.StateKVError, match="capture"):
+                h.decode(0, *many)
+    out.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert same(out, want)
+    h.decode(0, *many)                  # grows the scratch
+    one[0].mul_(2)
+    want = h.decode(0, *one)[0].clone()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert same(out, want)
+    h.close()

@@ -204,3 +204,12 @@ def test_binding_refusals():
             call()
     with pytest.raises(ValueError, match="dtype"):
         c.append(k.half(), k.half(), 0)
+
+
+def test_handle_refusals():
+    """A handle's 4-bit detailed state: what is refused without a device."""
+    S = _lib()
+    assert S.lib.statekv_set_detailed_format(None, 1) == -1
+    assert S.lib.statekv_get_detailed_q4(None, 0, None, None, None, None) == -1
+    with pytest.raises(ValueError, match="detailed"):
+        S.StateKV(4, 2, 64, 16, 32, 4, detailed="q8")
