@@ -4,9 +4,16 @@
 // With codes c, scales s and smallest values m per (token j, group g):
 //   q . k_j  = sum_g [ s_jg (q_g . c_jg) + m_jg sum(q_g) ],
 //   O        = sum_j p_j v_j = sum_j (p_j s_jg) (c_jg - 8) + sum_j p_j (m_jg + 8 s_jg).
-// The codes are exact fp16 numbers (an and-or gives a pair, with one rotation
-// for every four), so both sums are fp16 products with float32 accumulation, and the
-// scales meet float32 numbers only.  The rows are the G query heads of a KV
+// The codes are exact fp16 numbers, so both sums are fp16 products with float32
+// accumulation, and the scales meet float32 numbers only.  In bf16 calls a pair
+// of codes is one and of the word as it stands: in a half's low ten bits a code
+// is a subnormal number, c 2^-18 or c 2^-22, which the tensor cores take exactly;
+// Q (or P s) is 16 times larger where it meets the latter.  What the rounding of
+// P s to fp16 would do to a code of 15 is halved by centring: 8 sum(P s), of the
+// rounded P s, comes from one more product with a constant and is taken off at
+// the end.  Against codes c - 8 made by subtractions (float32 calls keep those:
+// sums of half the size) 71 -> 59 us for 4 streams of up to 131072 tokens, G = 7,
+// D = 128.  The rows are the G query heads of a KV
 // head times the text tokens, eight to a tile.
 //   Q: scaled by a power of two per row (largest element in [2^10, 2^11)); bf16
 //     values are then exact in fp16, float32 ones are split into two fp16 parts
@@ -15,7 +22,7 @@
 //     R_g per group, lazily raised as the row maximum is): 2^-11 off at most,
 //     an eighth of what the bf16 result rounds by; float32 again takes two parts.
 //   P: relative to a row maximum that moves only when a logit exceeds it by
-//     more than 2^8, so that most blocks need one vote and no shuffle.
+//     more than 2^6, so that most blocks need one vote and no shuffle.
 // Tensor-core shape m16n8k16 with tokens (K) or channels (V) as the 16 rows and
 // query rows as the 8 columns: the fragments come from shared memory as stored,
 // S^T turns into P^T's fragment by an 8x8 transpose, and nothing but 4-bit codes
@@ -38,11 +45,15 @@
 namespace skv {
 namespace {
 
-constexpr int kWarps = 12;
+// Warps of a worker: as many as their registers allow without spills.
+template <int NT, int NS>
+constexpr int warps_of() {
+  return NT * NS == 1 ? 12 : 8;
+}
 constexpr int kStages = 4;      // blocks in flight per warp
-constexpr float kRaise = 8.f;   // log2 headroom of the lazy row maximum
+constexpr float kRaise = 6.f;   // log2 headroom of the lazy row maximum
 constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
-constexpr float kPScale = 64.f; // P s <= 2^8 * 64 < 65504
+constexpr float kPScale = 512.f;    // P s <= 2^6 * 512 < 65504
 
 __device__ int g_err;  // first error of the ring's waits of all calls on a device
 
@@ -53,11 +64,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {  // c = A B
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -66,21 +83,34 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
-// The four fields of a word as fp16 pairs: c + 16, or c - 8.
+// The four fields of a word as fp16 pairs: c - 8, or, as they stand in the word,
+// the subnormal numbers c 2^-18 (fields 0, 3) and c 2^-22 (fields 1, 2).
 template <bool kCentred>
 __device__ __forceinline__ void codes_of(uint32_t x, uint32_t (&f)[4]) {
   const uint32_t y = q4_turn(x);
+  if (!kCentred) {
+    f[0] = x & 0x03C003C0u;
+    f[1] = y & 0x003C003Cu;
+    f[2] = x & 0x003C003Cu;
+    f[3] = y & 0x03C003C0u;
+    return;
+  }
   f[0] = q4_raw<0>(x);
   f[1] = q4_raw<1>(y);
   f[2] = q4_raw<2>(x);
   f[3] = q4_raw<3>(y);
-  if (kCentred) {
-    f[0] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[0]), __float2half2_rn(24.f)));
-    f[3] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[3]), __float2half2_rn(24.f)));
-  }
-  const __half2 off = __float2half2_rn(kCentred ? 264.f : 240.f);
-  f[1] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[1]), off));
-  f[2] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[2]), off));
+  const __half2 near = __float2half2_rn(24.f), far = __float2half2_rn(264.f);
+  f[0] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[0]), near));
+  f[1] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[1]), far));
+  f[2] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[2]), far));
+  f[3] = half2_bits(__hsub2(*reinterpret_cast<__half2*>(&f[3]), near));
+}
+
+// A token's scale words.
+template <int NG>
+__device__ __forceinline__ void scales_of(const uint8_t* scales, int tok, uint32_t (&sm)[NG]) {
+  if (NG == 2) *reinterpret_cast<uint2*>(sm) = *reinterpret_cast<const uint2*>(scales + tok * 8);
+  else sm[0] = *reinterpret_cast<const uint32_t*>(scales + tok * 4);
 }
 
 __device__ __forceinline__ void load_channels(const __nv_bfloat16* p, float (&x)[8]) {
@@ -124,13 +154,17 @@ __device__ __forceinline__ Deal deal_of(const WindowArgs& a, int W) {
 }
 
 template <typename T, int D, int NT, int NS>
-__global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
+__global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   using B = Q4Block<D>;
+  constexpr int kWarps = warps_of<NT, NS>();
   constexpr int NG = B::kGroups;
   constexpr int KW = D / 32;          // K words per (token row, tig)
   constexpr int MT = D / 16;          // 16-channel tiles of O
   constexpr int kRows = 8 * NT;
   constexpr int kStride = D + 4;      // padded row of the partials in shared memory
+  constexpr bool kCentred = NS == 2;  // codes as c - 8, else as subnormals
+  // S^T and O^T are in units of kUnit: with Q (P s) 16 times larger where the code is c 2^-22
+  constexpr float kCodeNear = 0x1p-18f, kCodeFar = 0x1p-22f, kUnit = kCentred ? 1.f : kCodeNear;
   extern __shared__ __align__(16) uint8_t smem[];
   const WindowArgs& a = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -227,15 +261,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const float x0 = qv[nt][w][q4_k_channel(f, 0)] * up, x1 = qv[nt][w][q4_k_channel(f, 1)] * up;
+          const float by = !kCentred && (f == 1 || f == 2) ? 16.f * up : up;
+          const float x0 = qv[nt][w][q4_k_channel(f, 0)] * by, x1 = qv[nt][w][q4_k_channel(f, 1)] * by;
           const __half2 hi = __floats2half2_rn(x0, x1);
           const float2 h = __half22float2(hi);
           qf[nt][0][2 * w + (f >> 1)][f & 1] = half2_bits(hi);
-          if (NS == 2) {
+          if (kCentred) {
             qf[nt][NS - 1][2 * w + (f >> 1)][f & 1] = half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y));
             sum[w >> 1] += x0 + x1;
           } else {
-            sum[w >> 1] += h.x + h.y;
+            sum[w >> 1] += (h.x + h.y) * (f == 1 || f == 2 ? kCodeFar : kCodeNear);
           }
         }
 #pragma unroll
@@ -254,7 +289,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       }
     }
 
-    float o[NT][MT][4], corr[NT][NG][2], l[NT][2], m[NT][2], vR[NG], vs[NG];
+    // o8: eight times the sum of P s as rounded, in O's fragment (all channels alike)
+    constexpr int NC = kCentred ? 0 : NG;
+    float o8[NT][NC + 1][4];
+    // m: row maximum in log2 units; mr: m, or 0 for -inf; above: the logit (before rs) that raises it
+    float o[NT][MT][4], corr[NT][NG][2], l[NT][2], m[NT][2], mr[NT][2], above[NT][2], vR[NG], vs[NG];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -262,9 +301,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][mt][e] = 0.f;
 #pragma unroll
+      for (int gg = 0; gg < NC; ++gg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o8[nt][gg][e] = 0.f;
+#pragma unroll
       for (int e = 0; e < 2; ++e) {
         l[nt][e] = 0.f;
-        m[nt][e] = -INFINITY;
+        m[nt][e] = above[nt][e] = -INFINITY;
+        mr[nt][e] = 0.f;
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] = 0.f;
       }
@@ -277,13 +321,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
 
     for (int v = v0 + warp; ok && v < v1; v += kWarps, ++done) {
       const int stage = done % kStages;
-      if (!(ok = tc::warp_wait(bars + 8u * stage, (done / kStages) & 1, &g_err, tc::kErrWaitLoad, abort_flag))) break;
+      const uint32_t bar = bars + 8u * stage, parity = (done / kStages) & 1;
+      if (!__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)) &&
+          !(ok = tc::warp_wait(bar, parity, &g_err, tc::kErrWaitLoad, abort_flag)))
+        break;
       const uint8_t* blk = ring + stage * B::kBytes;
       const int t0 = vis.block(v) * kQ4Tokens;
       bool full = t0 + kQ4Tokens <= vis.L;
       if (a.window)
-        full = full && ((long long)t0 > (long long)vis.L + i_last - a.window || t0 + kQ4Tokens <= a.n_sink);
-      // ---- S^T = K Q^T, 16 tokens at a time; t = logits in log2 units
+        full = full && (t0 > vis.L + i_last - a.window || t0 + kQ4Tokens <= a.n_sink);
+      // ---- S^T = K Q^T, 16 tokens at a time; t rs = logits in log2 units
       float t[NT][2][4];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
@@ -298,31 +345,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
         }
         float acc[NT][NG][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][gg][e] = 0.f;
-#pragma unroll
         for (int w = 0; w < KW; ++w) {
           uint32_t fa[4], fb[4];
-          codes_of<NS == 2>(ka[w], fa);
-          codes_of<NS == 2>(kb[w], fb);
+          codes_of<kCentred>(ka[w], fa);
+          codes_of<kCentred>(kb[w], fb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int ns = 0; ns < NS; ++ns) {
-              mma16816(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
+              if ((w & 1) == 0 && ns == 0)
+                mma16816_first(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
+              else
+                mma16816(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
               mma16816(acc[nt][w >> 1], fa[2], fb[2], fa[3], fb[3], qf[nt][ns][2 * w + 1][0], qf[nt][ns][2 * w + 1][1]);
             }
         }
-        const uint32_t* ks = reinterpret_cast<const uint32_t*>(blk + B::kKs) + (kt * 16 + gid) * NG;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t sms[NG];
+          scales_of(blk + B::kKs, kt * 16 + hh * 8 + gid, sms);
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) {
-            const uint32_t sm = ks[hh * 8 * NG + gg];
-            const float sc = q4_scale(sm), mid = fmaf(sc, NS == 2 ? 8.f : -16.f, q4_min(sm));
+            const uint32_t sm = sms[gg];
+            const float sc = q4_scale(sm), mid = kCentred ? fmaf(sc, 8.f, q4_min(sm)) : q4_min(sm);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -331,20 +376,29 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
                 t[nt][kt][hh * 2 + e] = fmaf(sc, acc[nt][gg][hh * 2 + e], sum);
               }
           }
+          if (!kCentred) {  // (in Q's factor or the scales 2^18 could overflow)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) t[nt][kt][hh * 2 + e] *= 1.f / kUnit;
+          }
+        }
       }
       // ---- V scales of this lane's tokens (t0 + 16 kt + 8 hh + gid)
       float sv[2][2][NG], mv[2][2][NG];
-      const uint32_t* vsp = reinterpret_cast<const uint32_t*>(blk + B::kVs);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t sms[NG];
+          scales_of(blk + B::kVs, kt * 16 + hh * 8 + gid, sms);
 #pragma unroll
           for (int gg = 0; gg < NG; ++gg) {
-            const uint32_t sm = vsp[(kt * 16 + hh * 8 + gid) * NG + gg];
+            const uint32_t sm = sms[gg];
             sv[kt][hh][gg] = q4_scale(sm);
             mv[kt][hh][gg] = fmaf(sv[kt][hh][gg], 8.f, q4_min(sm));
           }
+        }
       // ---- masks: hidden tokens get a logit of -inf; a V scale no row uses gets 0
       if (!full) {
 #pragma unroll
@@ -354,7 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             const int tok = t0 + kt * 16 + hh * 8 + gid;
             const bool in = tok < vis.L;
             const bool keep = !a.window || tok < a.n_sink;
-            if (!(in && (keep || (long long)tok > (long long)vis.L + i_first - a.window))) {
+            if (!(in && (keep || tok > vis.L + i_first - a.window))) {
 #pragma unroll
               for (int gg = 0; gg < NG; ++gg) sv[kt][hh][gg] = mv[kt][hh][gg] = 0.f;
             }
@@ -362,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const bool ok = in && (keep || (long long)tok > (long long)vis.L + irow[nt][e] - a.window);
+                const bool ok = in && (keep || tok > vis.L + irow[nt][e] - a.window);
                 if (!ok) t[nt][kt][hh * 2 + e] = -INFINITY;
               }
           }
@@ -375,9 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
         for (int e = 0; e < 2; ++e) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float& x_ = t[nt][c >> 1][(c & 1) * 2 + e];
-            x_ *= rs[nt][e];
-            raise |= x_ > m[nt][e] + kRaise;
+            raise |= t[nt][c >> 1][(c & 1) * 2 + e] > above[nt][e];
           }
         }
 #pragma unroll
@@ -392,9 +444,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
             float top = fmaxf(fmaxf(t[nt][0][e], t[nt][0][2 + e]), fmaxf(t[nt][1][e], t[nt][1][2 + e]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float nm = fmaxf(m[nt][e], top);
+            const float nm = fmaxf(m[nt][e], top * rs[nt][e]);
             fo[nt][e] = nm == m[nt][e] ? 1.f : tc::ex2_approx(m[nt][e] - nm);
             m[nt][e] = nm;
+            mr[nt][e] = nm == -INFINITY ? 0.f : nm;
+            above[nt][e] = (nm + kRaise) / rs[nt][e];
             l[nt][e] *= fo[nt][e];
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] *= fo[nt][e];
@@ -416,23 +470,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][mt][e] *= fo[nt][e & 1] * fv[mt / 4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gg = 0; gg < NC; ++gg)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o8[nt][gg][e] *= fo[nt][e & 1] * fv[gg];
       }
       // ---- P, its sums, and P s as fp16 fragments
       uint32_t pf[NT][NS][NG][2][2];
       auto weights = [&](auto careful) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
           for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = tc::ex2_approx(t[nt][kt][hh * 2] - m0), p1 = tc::ex2_approx(t[nt][kt][hh * 2 + 1] - m1);
+              const float p0 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2], rs[nt][0], -mr[nt][0]));
+              const float p1 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2 + 1], rs[nt][1], -mr[nt][1]));
               l[nt][0] += p0;
               l[nt][1] += p1;
 #pragma unroll
               for (int gg = 0; gg < NG; ++gg) {
-                float s0 = sv[kt][hh][gg] * vs[gg], s1 = s0, m0v = mv[kt][hh][gg], m1v = m0v;
+                // tokens of fields 0 and 3 (kt == hh): 16 times less
+                float s0 = sv[kt][hh][gg] * (!kCentred && kt == hh ? vs[gg] * (kCodeFar / kCodeNear) : vs[gg]), s1 = s0, m0v = mv[kt][hh][gg], m1v = m0v;
                 if (careful) {  // (the same roundings with and without)
                   if (t[nt][kt][hh * 2] == -INFINITY) s0 = m0v = 0.f;
                   if (t[nt][kt][hh * 2 + 1] == -INFINITY) s1 = m1v = 0.f;
@@ -463,7 +524,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
       }
       if (odd) weights(std::true_type());
       else weights(std::false_type());
-      // ---- O^T += V^T P^T, 32 channels at a time
+      // ---- the weights' own sums, then O^T += V^T P^T, 32 channels at a time
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int gg = 0; gg < NC; ++gg) {
+          constexpr uint32_t near8 = 0x02000200u, far8 = 0x00200020u;  // code 8
+          mma16816(o8[nt][gg], near8, near8, far8, far8, pf[nt][0][gg][0][0], pf[nt][0][gg][0][1]);
+          mma16816(o8[nt][gg], far8, far8, near8, near8, pf[nt][0][gg][1][0], pf[nt][0][gg][1][1]);
+        }
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         const uint4 w = *reinterpret_cast<const uint4*>(blk + B::kV + c * 512 + lane * 16);
@@ -472,8 +541,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
         for (int half = 0; half < 2; ++half) {
           const uint32_t x0 = half ? w.z : w.x, x1 = half ? w.w : w.y;
           uint32_t fa[4], fb[4];
-          codes_of<true>(x0, fa);
-          codes_of<true>(x1, fb);
+          codes_of<kCentred>(x0, fa);
+          codes_of<kCentred>(x1, fb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -521,7 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           wo[(warp * kRows + nt * 8 + 2 * tig + (e & 1)) * kStride + mt * 16 + (e >> 1) * 8 + gid] =
-              fmaf(o[nt][mt][e], vR[mt / 4] * (1.f / kPScale), corr[nt][mt / 4][e & 1]);
+              fmaf((kCentred ? o[nt][mt][e] : o[nt][mt][e] - o8[nt][kCentred ? 0 : mt / 4][e]) * (1.f / (kPScale * (kCentred ? 1.f : kCodeFar))), vR[mt / 4], corr[nt][mt / 4][e & 1]);
     }
     __syncthreads();
     const long long part = (long long)blockIdx.y * (p.W + a.S * a.Hkv) + blockIdx.x + s * a.Hkv + g;
@@ -677,6 +746,7 @@ cudaError_t launch_merge(const Q4AttnArgs& p, cudaStream_t st) {
 template <typename T, int D, int NT, int NS>
 cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
   using B = Q4Block<D>;
+  constexpr int kWarps = warps_of<NT, NS>();
   constexpr int ring = kWarps * kStages * B::kBytes;
   constexpr int merge = kWarps * 8 * NT * (D + 4 + 2) * 4;
   constexpr int smem = ring > merge ? ring : merge;
