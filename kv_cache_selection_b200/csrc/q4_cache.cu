@@ -61,23 +61,31 @@ __device__ __forceinline__ float round_scale(float hi, float m) {
   return __uint_as_float(bits);
 }
 
-// The integer nearest to (x - m) / s, ties to even, from c at most 1 away: the
-// remainder x - m - c s is exact in float32 (it is at most s and a multiple of
-// the last place of x - m), so its place against s / 2 is, too.
-__device__ __forceinline__ float settle(float x, float m, float s, float c) {
+// What to add to c, at most 1 away from it, for the integer nearest to
+// (x - m) / s, ties to even: the remainder x - m - c s is exact in float32 (it is
+// at most s and a multiple of the last place of x - m), so its place against
+// s / 2 is, too.
+__device__ __forceinline__ int settle(float x, float m, float s, int c) {
   float rest;
   const float d = exact_difference(x, m, rest);
-  const float e = fmaf(-c, s, d), half = 0.5f * s;
-  const bool odd = (int)c & 1;
-  if (e > half || (e == half && (rest > 0.f || (rest == 0.f && odd)))) return c + 1.f;
-  if (e < -half || (e == -half && (rest < 0.f || (rest == 0.f && odd)))) return c - 1.f;
-  return c;
+  const float e = fmaf(-(float)c, s, d), half = 0.5f * s;
+  const bool odd = c & 1;
+  if (e > half || (e == half && (rest > 0.f || (rest == 0.f && odd)))) return 1;
+  if (e < -half || (e == -half && (rest < 0.f || (rest == 0.f && odd)))) return -1;
+  return 0;
+}
+// x[e]
+__device__ __forceinline__ float pick(const float (&x)[8], int e) {
+  const bool b0 = e & 1, b1 = e & 2, b2 = e & 4;
+  const float p = b0 ? x[1] : x[0], q = b0 ? x[3] : x[2], r = b0 ? x[5] : x[4], t = b0 ? x[7] : x[6];
+  const float u = b1 ? q : p, v = b1 ? t : r;
+  return b2 ? v : u;
 }
 
-// Smallest and largest of the eight lanes that hold a group, NaN if any is one.
+// Smallest and largest of the four lanes that hold a group, NaN if any is one.
 __device__ __forceinline__ void group_range(float& lo, float& hi) {
 #pragma unroll
-  for (int off = 1; off < 8; off <<= 1) {
+  for (int off = 1; off < 4; off <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
   }
@@ -93,16 +101,19 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Eight channels as loaded, as float32, and the range of their group.
+// Sixteen channels as loaded, as float32 (eight of them), and the range of their group.
 template <typename T>
-struct Raw8;
+struct Raw16;
 template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { r = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw16<__nv_bfloat16> {
+  uint4 r[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    r[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    r[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { r[0] = r[1] = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(int half, float (&x)[8]) const {
+    const uint32_t w[4] = {r[half].x, r[half].y, r[half].z, r[half].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
@@ -111,48 +122,70 @@ struct Raw8<__nv_bfloat16> {
   }
   // (smallest, -largest) as one bf16 pair: one shuffle a step for both
   __device__ __forceinline__ void range(float& lo, float& hi) const {
-    const uint32_t mn = min2_nan(min2_nan(r.x, r.y), min2_nan(r.z, r.w)), mx = max2_nan(max2_nan(r.x, r.y), max2_nan(r.z, r.w));
+    const uint32_t mn = min2_nan(min2_nan(min2_nan(r[0].x, r[0].y), min2_nan(r[0].z, r[0].w)),
+                                 min2_nan(min2_nan(r[1].x, r[1].y), min2_nan(r[1].z, r[1].w)));
+    const uint32_t mx = max2_nan(max2_nan(max2_nan(r[0].x, r[0].y), max2_nan(r[0].z, r[0].w)),
+                                 max2_nan(max2_nan(r[1].x, r[1].y), max2_nan(r[1].z, r[1].w)));
     uint32_t p = min2_nan(__byte_perm(mn, mx, 0x5410) ^ 0x80000000u, __byte_perm(mn, mx, 0x7632) ^ 0x80000000u);
 #pragma unroll
-    for (int off = 1; off < 8; off <<= 1) p = min2_nan(p, __shfl_xor_sync(0xffffffffu, p, off));
+    for (int off = 1; off < 4; off <<= 1) p = min2_nan(p, __shfl_xor_sync(0xffffffffu, p, off));
     lo = __uint_as_float(p << 16);
     hi = __uint_as_float((p & 0xffff0000u) ^ 0x80000000u);
   }
 };
 template <>
-struct Raw8<float> {
-  float4 a, b;
+struct Raw16<float> {
+  float4 r[4];
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void get(int half, float (&x)[8]) const {
+    const float4 a = r[2 * half], b = r[2 * half + 1];
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
   __device__ __forceinline__ void range(float& lo, float& hi) const {
-    lo = min_nan(min_nan(min_nan(a.x, a.y), min_nan(a.z, a.w)), min_nan(min_nan(b.x, b.y), min_nan(b.z, b.w)));
-    hi = max_nan(max_nan(max_nan(a.x, a.y), max_nan(a.z, a.w)), max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)));
+    lo = hi = r[0].x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo = min_nan(lo, min_nan(min_nan(r[i].x, r[i].y), min_nan(r[i].z, r[i].w)));
+      hi = max_nan(hi, max_nan(max_nan(r[i].x, r[i].y), max_nan(r[i].z, r[i].w)));
+    }
     group_range(lo, hi);
   }
 };
 
-// Codes of eight channels as nibbles (channel e at bits 4e), from the range of
-// their group; sm becomes the packed (s, m).  y = (x - m) * (1/s) in float32 is
-// off by less than 2^-17 (a quotient of at most 15, five half steps of relative
-// 2^-24); only where that could change the nearest integer is the code settled
-// exactly.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, float hi, uint32_t& sm) {
+// Smallest value and scale of a group.
+struct Scale {
+  float m, s, r;     // r: about 1 / s, 0 where s is not above 0
+  bool bad, small;   // not finite; s too far from 1 for r
+  __device__ __forceinline__ uint32_t packed() const {
+    return bad ? 0x7fc07fc0u : (__float_as_uint(s) >> 16) | __float_as_uint(m);
+  }
+};
+__device__ __forceinline__ Scale scale_of(float lo, float hi) {
+  Scale g;
   uint32_t mb = __float_as_uint(lo);  // rounded down to bfloat16 on the bit pattern
   if ((mb & 0xffffu) && (mb >> 31)) mb += 0x10000u;
-  mb &= 0xffff0000u;
-  const float m = __uint_as_float(mb);
-  const bool bad = !(fabsf(hi) < INFINITY && fabsf(m) < INFINITY);
-  const float s = round_scale(hi, m);
-  sm = bad ? 0x7fc07fc0u : (__float_as_uint(s) >> 16) | mb;
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  if (!(s > 0.f)) r = 0.f;
+  g.m = __uint_as_float(mb & 0xffff0000u);
+  g.bad = !(fabsf(hi) < INFINITY && fabsf(g.m) < INFINITY);
+  g.s = round_scale(hi, g.m);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.r) : "f"(g.s));
+  if (!(g.s > 0.f)) g.r = 0.f;
+  g.small = g.s > 0.f && !(g.s >= 0x1p-100f && g.s <= 0x1p100f);
+  return g;
+}
+
+// Codes of eight channels as nibbles (channel e at bits 4e).  y = (x - m) * (1/s)
+// in float32 is off by less than 2^-17 (a quotient of at most 15, five half steps
+// of relative 2^-24); only where that could change the nearest integer is the
+// code settled exactly.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], const Scale& g) {
+  const float m = g.m, s = g.s, r = g.r;
   const float2 r2 = make_float2(r, r), nm2 = make_float2(-m, -m), magic = make_float2(12582912.f, 12582912.f);
   const float2 unmagic = make_float2(-12582912.f, -12582912.f);
   float far = 0.f;  // distance from the nearest integer
@@ -169,18 +202,18 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, flo
     y[2 * i + 1] = e.y;
     far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
   }
-  const bool small = s > 0.f && !(s >= 0x1p-100f && s <= 0x1p100f);
-  if ((far > 0.5f - 0x1p-17f || small) && !bad) {
-    if (small) {
+  // four codes as one float32 integer below 2^16, exactly
+  float2 w = make_float2(c[3], c[7]);
+#pragma unroll
+  for (int e = 2; e >= 0; --e) w = tc::ffma2(w, make_float2(16.f, 16.f), make_float2(c[e], c[e + 4]));
+  w = tc::fadd2(w, make_float2(8388608.f, 8388608.f));
+  uint32_t word = __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
+  if ((far > 0.5f - 0x1p-17f || g.small) && !g.bad) {
+    if (g.small) {
+      word = 0;
 #pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        float v = x[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
-        v = (float)min(15, max(0, (int)rint(((double)v - (double)m) / (double)s)));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = e == k ? v : c[k];
-      }
+      for (int e = 0; e < 8; ++e)
+        word |= (uint32_t)min(15, max(0, (int)rint(((double)pick(x, e) - (double)m) / (double)s))) << (4 * e);
     } else {
       uint32_t todo = 0;
 #pragma unroll
@@ -188,24 +221,11 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float lo, flo
       while (todo) {  // rarely more than one
         const int e = __ffs(todo) - 1;
         todo &= todo - 1;
-        float v = x[0], n = c[0];
-#pragma unroll
-        for (int k = 1; k < 8; ++k) {
-          v = e == k ? x[k] : v;
-          n = e == k ? c[k] : n;
-        }
-        n = settle(v, m, s, n);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = e == k ? n : c[k];
+        word += (uint32_t)settle(pick(x, e), m, s, (int)(word >> (4 * e) & 15u)) << (4 * e);
       }
     }
   }
-  // four codes as one float32 integer below 2^16, exactly
-  float2 w = make_float2(c[3], c[7]);
-#pragma unroll
-  for (int e = 2; e >= 0; --e) w = tc::ffma2(w, make_float2(16.f, 16.f), make_float2(c[e], c[e + 4]));
-  w = tc::fadd2(w, make_float2(8388608.f, 8388608.f));
-  return __byte_perm(__float_as_uint(w.x), __float_as_uint(w.y), 0x5410);
+  return word;
 }
 
 // 8 x 8 nibbles transposed: nibble e of row n -> nibble n of row e
@@ -232,22 +252,23 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&a)[8]) {
   }
 }
 
-// Append.  A lane quantises eight channels of a token's key or value, D/8 lanes
-// a token, with the next two tokens' loads in flight.  Eight channels of a key are one
-// word of the block; values go through shared memory as nibbles, where a thread
-// transposes eight tokens x eight channels into V's words.  The block's image
-// leaves as 16-byte stores.
+// Append.  A lane quantises sixteen channels of a token's key or value, D/16
+// lanes a token, with the next token's loads in flight (with eight channels a
+// lane the group's range and scale, which each of its lanes computes, cost as
+// much as the codes).  Eight channels of a key are one word of the block; values
+// go through shared memory as nibbles, where a thread transposes eight tokens x
+// eight channels into V's words.  The block's image leaves as 16-byte stores.
 constexpr int kAppendThreads = 128;
 template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) q4_append_kernel(Q4IoArgs a) {
   using B = Q4Block<D>;
-  constexpr int kRowLanes = D / 8;                       // lanes of a token
+  constexpr int kUnits = D / 8;                            // eight-channel units of a token
+  constexpr int kRowLanes = D / 16;                        // lanes of a token
   constexpr int kRowsAtOnce = kAppendThreads / kRowLanes;  // tokens per pass of the block
   constexpr int kPasses = 2 * kQ4Tokens / kRowsAtOnce;
-  constexpr int kBatch = 2;
-  static_assert(kPasses / 2 % kBatch == 0, "a batch is all keys or all values");
+  static_assert(kPasses % 2 == 0, "a pass is all keys or all values");
   __shared__ __align__(16) uint8_t image[B::kBytes];
-  __shared__ uint32_t vn[kQ4Tokens][kRowLanes + 1];      // nibbles of the values
+  __shared__ uint32_t vn[kQ4Tokens][kUnits + 1];      // nibbles of the values
   pdl_wait();
   pdl_trigger();
   const int sg = blockIdx.x / a.n_blk, s = sg / a.Hkv, g = sg % a.Hkv;
@@ -255,48 +276,47 @@ __global__ void __launch_bounds__(kAppendThreads) q4_append_kernel(Q4IoArgs a) {
   const int b = sp.p0 / kQ4Tokens + blockIdx.x % a.n_blk;
   if ((long long)b * kQ4Tokens >= sp.p1 || sp.p0 >= sp.p1) return;
   const int t_lo = max(sp.p0 - b * kQ4Tokens, 0), t_hi = min(sp.p1 - b * kQ4Tokens, kQ4Tokens);
-  const int c8 = threadIdx.x % kRowLanes, r_of = threadIdx.x / kRowLanes;
+  const int c16 = threadIdx.x % kRowLanes, r_of = threadIdx.x / kRowLanes;
   // rows 0..31 keys, 32..63 values; this thread's token of pass p is
   // (p % (kPasses / 2)) * kRowsAtOnce + r_of
-  const long long first = (((long long)s * a.n + (long long)b * kQ4Tokens - sp.start + r_of) * a.Hkv + g) * D + c8 * 8;
+  const long long first = (((long long)s * a.n + (long long)b * kQ4Tokens - sp.start + r_of) * a.Hkv + g) * D + c16 * 16;
   const T* k_row = static_cast<const T*>(a.k) + first;
   const T* v_row = static_cast<const T*>(a.v) + first;
   const long long pass_stride = (long long)kRowsAtOnce * a.Hkv * D;
-  uint32_t* k_word = reinterpret_cast<uint32_t*>(image + r_of * B::kRow + ((c8 % 8) / 2) * (D / 8) + ((c8 / 8) * 2 + c8 % 2) * 4);
-  Raw8<T> next[kBatch];
-  auto fetch = [&](int p0) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int p = (p0 + i) % (kPasses / 2), t = p * kRowsAtOnce + r_of;
-      if (t >= t_lo && t < t_hi) next[i].load((p0 >= kPasses / 2 ? v_row : k_row) + p * pass_stride);
-      else next[i].zero();
-    }
+  // the two words of a lane's sixteen key channels are neighbours
+  uint8_t* k_word = image + r_of * B::kRow + (c16 % 4) * (D / 8) + (c16 / 4) * 8;
+  Raw16<T> next;
+  auto fetch = [&](int p) {
+    const int pp = p % (kPasses / 2), t = pp * kRowsAtOnce + r_of;
+    if (t >= t_lo && t < t_hi) next.load((p >= kPasses / 2 ? v_row : k_row) + pp * pass_stride);
+    else next.zero();
   };
   fetch(0);
 #pragma unroll 1
-  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
-    const bool is_v = p0 >= kPasses / 2;
-    float x[kBatch][8], lo[kBatch], hi[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      next[i].get(x[i]);
-      next[i].range(lo[i], hi[i]);
+  for (int p = 0; p < kPasses; ++p) {
+    const bool is_v = p >= kPasses / 2;
+    const int t0 = p % (kPasses / 2) * kRowsAtOnce;
+    const Raw16<T> now = next;
+    if (p + 1 < kPasses) fetch(p + 1);
+    float lo, hi, x[8];
+    now.range(lo, hi);
+    const Scale sc = scale_of(lo, hi);
+    now.get(0, x);
+    const uint32_t w0 = quantise8(x, sc);
+    now.get(1, x);
+    const uint32_t w1 = quantise8(x, sc);
+    if (is_v) {
+      vn[t0 + r_of][2 * c16] = w0;
+      vn[t0 + r_of][2 * c16 + 1] = w1;
+    } else {
+      *reinterpret_cast<uint2*>(k_word + t0 * B::kRow) = make_uint2(q4_rotate(w0), q4_rotate(w1));
     }
-    if (p0 + kBatch < kPasses) fetch(p0 + kBatch);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int t0 = (p0 + i) % (kPasses / 2) * kRowsAtOnce;
-      uint32_t sm;
-      const uint32_t w = quantise8(x[i], lo[i], hi[i], sm);
-      if (is_v) vn[t0 + r_of][c8] = w;
-      else k_word[t0 * (B::kRow / 4)] = q4_rotate(w);
-      if (c8 % 8 == 0)
-        reinterpret_cast<uint32_t*>(image + (is_v ? B::kVs : B::kKs))[(t0 + r_of) * B::kGroups + c8 / 8] = sm;
-    }
+    if (c16 % 4 == 0)
+      reinterpret_cast<uint32_t*>(image + (is_v ? B::kVs : B::kKs))[(t0 + r_of) * B::kGroups + c16 / 4] = sc.packed();
   }
   __syncthreads();
-  if (threadIdx.x < kRowLanes * 4) {
-    const int j = threadIdx.x % kRowLanes, tig = threadIdx.x / kRowLanes;
+  if (threadIdx.x < kUnits * 4) {
+    const int j = threadIdx.x % kUnits, tig = threadIdx.x / kUnits;
     uint32_t w[8];
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
