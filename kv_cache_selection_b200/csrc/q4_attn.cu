@@ -322,9 +322,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     for (int v = v0 + warp; ok && v < v1; v += kWarps, ++done) {
       const int stage = done % kStages;
       const uint32_t bar = bars + 8u * stage, parity = (done / kStages) & 1;
-      if (!__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)) &&
-          !(ok = tc::warp_wait(bar, parity, &g_err, tc::kErrWaitLoad, abort_flag)))
-        break;
+      if (!(ok = tc::warp_wait_all(bar, parity, &g_err, tc::kErrWaitLoad, abort_flag))) break;
       const uint8_t* blk = ring + stage * B::kBytes;
       const int t0 = vis.block(v) * kQ4Tokens;
       bool full = t0 + kQ4Tokens <= vis.L;

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     const int end = min((t_begin + n) * 4, vis.count()) * kQ4Tokens;
     const int mine = warp < 12 ? threadIdx.x - 32 : threadIdx.x - 160;  // 480 threads
     using Words = typename std::conditional<NG == 2, uint2, uint32_t>::type;
-#pragma unroll 4
+#pragma unroll 8
     for (int x = t_begin * 4 * kQ4Tokens + mine; x < end; x += 480) {
       const Token t = token_of(a, vis, x / kQ4Tokens, x % kQ4Tokens, i_first, i_last);
       const uint8_t* blk = base + (long long)vis.block(x / kQ4Tokens) * B::kBytes + (x % kQ4Tokens) * (NG * 4);
@@ -247,41 +247,44 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     const int tid = threadIdx.x - 384, row = row0 + tid, rr = min(row, R - 1);
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                     (((long long)s * a.n + rr / G) * a.Hq + g * G + rr % G) * D);
-    uint4 x[D / 8];
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) x[c] = __ldg(q + c);
+    // read twice, eight chunks at a time (all of them in registers would spill)
     float top = 0.f;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c)
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = __ldg(q + c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(&x[c])[e];
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&x)[e];
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
       }
+    }
     int ex = (int)(__float_as_uint(top) >> 23);
     ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, 12);
     const float up = row < R ? __uint_as_float((uint32_t)(264 - ex) << 23) : 0.f;
     reinterpret_cast<float*>(smem + L::kRow)[tid] = __uint_as_float((uint32_t)(ex - 10) << 23) * a.scale_log2;
-    float sum[NG];
+#pragma unroll 1
+    for (int gg = 0; gg < NG; ++gg) {
+      float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      float y[8], t = 0.f;
+      for (int c = 0; c < 8; ++c) {
+        const uint4 x = __ldg(q + gg * 8 + c);
+        float y[8], t = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(&x[c])[e];
-        y[2 * e] = __uint_as_float(w << 16) * up;
-        y[2 * e + 1] = __uint_as_float(w & 0xffff0000u) * up;
-        t += y[2 * e] + y[2 * e + 1];
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(&x)[e];
+          y[2 * e] = __uint_as_float(w << 16) * up;
+          y[2 * e + 1] = __uint_as_float(w & 0xffff0000u) * up;
+          t += y[2 * e] + y[2 * e + 1];
+        }
+        sum += t;
+        uint4 o;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          reinterpret_cast<uint32_t*>(&o)[f] = pack_half2(y[q4_k_channel(f, 0)], y[q4_k_channel(f, 1)]);
+        *reinterpret_cast<uint4*>(smem + L::kQ + gg * L::kAtom + tid * 128 + ((c ^ (tid & 7)) << 4)) = o;
       }
-      sum[c >> 3] = (c & 7) ? sum[c >> 3] + t : t;
-      uint4 o;
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        reinterpret_cast<uint32_t*>(&o)[f] = pack_half2(y[q4_k_channel(f, 0)], y[q4_k_channel(f, 1)]);
-      *reinterpret_cast<uint4*>(smem + L::kQ + (c >> 3) * L::kAtom + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) = o;
+      reinterpret_cast<float*>(smem + L::kQs)[tid * NG + gg] = sum;
     }
-#pragma unroll
-    for (int gg = 0; gg < NG; ++gg) reinterpret_cast<float*>(smem + L::kQs)[tid * NG + gg] = sum[gg];
     for (int b = 0; b < 2; ++b)  // the unused half of the depth-16 rows
       *reinterpret_cast<uint4*>(smem + L::kKx + b * 4096 + 2048 + tid * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async();
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       if (lane == 0) mbar_arrive(qx_full);
     }
     for (int j = 0; j < n; ++j) {
-      if (ok) ok = warp_wait(s_full(j & 1), (j >> 1) & 1, err, kErrWaitAcc, abort_flag);
+      if (ok) ok = warp_wait_all(s_full(j & 1), (j >> 1) & 1, err, kErrWaitAcc, abort_flag);
       fence_after_sync();
       const uint32_t t_s = t_lane + col_s(j & 1) + half * 64;
       const int v0 = (t_begin + j) * 4;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
         full = full && ((long long)vis.block(v0) * kQ4Tokens > (long long)vis.L + i_last - a.window ||
                         vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= a.n_sink);
       // V's poison words come with its tile
-      if (ok && !full) ok = warp_wait(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag);
+      if (ok && !full) ok = warp_wait_all(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag);
       if (!full) {  // hidden columns of S become -inf in tensor memory
         const long long from = a.window ? (long long)vis.L + i - a.window + 1 : 0;
 #pragma unroll 1
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
         if (raise) m_used = m_new;
         if (j > 0) {
           // O must hold every earlier tile's P V
-          if (!(ok = warp_wait(pv_done, (j - 1) & 1, err, kErrWaitAcc, abort_flag))) continue;
+          if (!(ok = warp_wait_all(pv_done, (j - 1) & 1, err, kErrWaitAcc, abort_flag))) continue;
           fence_after_sync();
           for (int c0 = 0; c0 < D / 64; ++c0) {
             uint32_t v[32];
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full(j & 1));
     }
-    if (ok) ok = warp_wait(o_done, 0, err, kErrWaitAcc, abort_flag);
+    if (ok) ok = warp_wait_all(o_done, 0, err, kErrWaitAcc, abort_flag);
     ok = ok && !*abort_flag;
     // l of the row's two halves
     half_max[half * 128 + r] = l;
@@ -522,9 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     for (int j = 0; j < n; ++j) {
       const int sl = j % kRaw, b2 = j & 1;
       // the row scales and sums of q lie in the second K tile until they are read
-      if (j == 1 && !warp_wait(qx_full, 0, err, kErrWaitLoad, abort_flag)) break;
-      if (!warp_wait(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
-      if (!warp_wait(k_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
+      if (j == 1 && !warp_wait_all(qx_full, 0, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait_all(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait_all(k_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
       const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
       const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);
       uint32_t s2[NG], x[4] = {0, 0, 0, 0};
@@ -574,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     const float norm = exp2i(-eV);
     for (int j = 0; j < n; ++j) {
       const int sl = j % kRaw, b2 = j & 1;
-      if (!warp_wait(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
-      if (!warp_wait(v_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
+      if (!warp_wait_all(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
+      if (!warp_wait_all(v_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
       const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
       uint8_t* tab = smem + L::kTab + w4 * (4 * NG * 32);  // [tig][group][f] (s pair, m + 8 s pair) of the warp's block
       const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);

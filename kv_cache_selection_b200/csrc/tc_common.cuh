@@ -311,6 +311,26 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// The same wait with every lane polling: for warps whose lanes work in step
+// afterwards.  (After warp_wait has had to wait, lane 0 was seen to run on apart
+// from the others up to the next warp barrier, at twice the instructions.)
+__device__ __forceinline__ bool warp_wait_all(uint32_t bar, uint32_t parity, int* err, int code,
+                                              volatile int* abort_flag, unsigned long long limit_ns = kWaitLimitNs) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 15u) == 0) {
+      const bool late = globaltimer_ns() - t0 > limit_ns;
+      if (__any_sync(0xffffffffu, late || *abort_flag)) {
+        if (late && (threadIdx.x & 31) == 0) atomicCAS(err, 0, code);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
