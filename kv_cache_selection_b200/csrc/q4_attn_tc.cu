@@ -7,7 +7,7 @@
 // 128-token key tiles.  Per key tile
 //   raw blocks -> shared memory          one warp, bulk copies into a ring
 //   K, V -> fp16 in shared memory        a warpgroup each
-//   S = Q K^T, O += P V                  one thread; tcgen05, fp16 in, float32 accumulate
+//   S = Q K^T, O += P V                  one warp; tcgen05, fp16 in, float32 accumulate
 //   P = 2^(S c - m)                      two warpgroups, thread = 64 columns of a row
 // with S double-buffered in tensor memory.  The two halves of a row share its
 // lazy maximum: one barrier a tile tells whether either wants to raise it.
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------ MMA issuer
-      if (lane == 0 && n > 0) {
+      if (n > 0) {
         constexpr uint32_t id_s = idesc_f16(128, 128), id_o = idesc_f16(128, D);
         const uint64_t dq = sdesc_sw128(sb + L::kQ, 16, 1024), dk = sdesc_sw128(sb + L::kK, 16, 1024);
         const uint64_t dv = sdesc_sw128(sb + L::kV, 16, 1024), dx = sdesc_plain(sb + L::kKx, 2048, 128);
@@ -319,38 +319,38 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (uint64_t)(((kk >> 2) * L::kAtom + (kk & 3) * 32) >> 4);
-            mma_ss(tmem + col_s(j & 1), dq + off, k0 + off, id_s, kk > 0 ? 1u : 0u);
+            mma_ss_e(tmem + col_s(j & 1), dq + off, k0 + off, id_s, kk > 0 ? 1u : 0u);
           }
-          mma_ts(tmem + col_s(j & 1), tmem + kColQx, dx + (uint64_t)((j & 1) * (4096 >> 4)), id_s, 1u);
-          mma_commit(s_full(j & 1));
-          mma_commit(k_empty(j & 1));
+          mma_ts_e(tmem + col_s(j & 1), tmem + kColQx, dx + (uint64_t)((j & 1) * (4096 >> 4)), id_s, 1u);
+          commit_e(s_full(j & 1));
+          commit_e(k_empty(j & 1));
         };
-        bool ok = mbar_wait(qx_full, 0, err, kErrWaitLoad, abort_flag) &&
-                  mbar_wait(k_full(0), 0, err, kErrWaitLoad, abort_flag);
+        bool ok = warp_spin_wait(qx_full, 0, err, kErrWaitLoad, abort_flag) &&
+                  warp_spin_wait(k_full(0), 0, err, kErrWaitLoad, abort_flag);
         if (ok) {
           fence_after_sync();
           issue_s(0);
         }
         for (int j = 0; ok && j < n; ++j) {
           if (j + 1 < n) {  // S(j+1) overwrites P(j-1), which P V(j-1), issued before, has read
-            if (!(ok = mbar_wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1, err, kErrWaitLoad, abort_flag))) break;
+            if (!(ok = warp_spin_wait(k_full((j + 1) & 1), ((j + 1) >> 1) & 1, err, kErrWaitLoad, abort_flag))) break;
             fence_after_sync();
             issue_s(j + 1);
           }
-          if (!(ok = mbar_wait(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag))) break;
-          if (!(ok = mbar_wait(p_full(j & 1), (j >> 1) & 1, err, kErrWaitP, abort_flag))) break;
+          if (!(ok = warp_spin_wait(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag))) break;
+          if (!(ok = warp_spin_wait(p_full(j & 1), (j >> 1) & 1, err, kErrWaitP, abort_flag))) break;
           fence_after_sync();
           const uint64_t v0 = dv + (uint64_t)((j & 1) * (2 * L::kVAtom >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + kColO, tmem + col_s(j & 1) + (kk >> 2) * 64 + (kk & 3) * 8, v0 + (uint64_t)(((kk >> 2) * L::kVAtom + (kk & 3) * 32) >> 4),
+            mma_ts_e(tmem + kColO, tmem + col_s(j & 1) + (kk >> 2) * 64 + (kk & 3) * 8, v0 + (uint64_t)(((kk >> 2) * L::kVAtom + (kk & 3) * 32) >> 4),
                    id_o, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(pv_done);
-          mma_commit(v_empty(j & 1));
-          if (j == n - 1) mma_commit(o_done);
+          commit_e(pv_done);
+          commit_e(v_empty(j & 1));
+          if (j == n - 1) commit_e(o_done);
         }
-        mma_commit(all_done);
-        drain_wait(all_done, 0, err);
+        commit_e(all_done);
+        if (lane == 0) drain_wait(all_done, 0, err);
       }
       __syncwarp();
     }
