@@ -27,6 +27,8 @@
 //
 // Warps (384 threads): 0 TMA producer, 1 tensor-memory owner and MMA issuer,
 // 4..7 softmax of tile A, 8..11 of tile B.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
@@ -231,63 +233,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait_slot = [&](int pos) {
         return warp_spin_wait(bar_full(pos % kSlots), (pos / kSlots) & 1, err, kErrWaitLoad, abort_flag);
       };
-      // query tile and key tile of S(q)
-      auto x_of = [&](int q) { return nB > 0 && (q >= 2 * nA || (q & 1)) ? 1 : 0; };
-      auto j_of = [&](int q) { return nB > 0 ? min(q >> 1, nA) : q; };
-      struct Next {  // S(q) = Q_x K_j^T
-        uint64_t dq, dk;
-        uint32_t s;
-      };
-      auto next_s = [&](int q) {
-        return Next{dq0 + (uint64_t)((x_of(q) * L::kTile) >> 4), dk0 + slot16(pos_k(j_of(q))), tmem + col_s(q % kS)};
-      };
-      auto issue_s = [&](Next n) {
-        asm volatile("" : "+l"(n.dq), "+l"(n.dk));  // the sums below stay here: hoisted, they would not fit the registers
+      auto slot_ready = [&](int pos) { return mbar_test_wait(bar_full(pos % kSlots), (pos / kSlots) & 1); };
+      // S = Q_x K_j^T into buffer b; last: no other tile of queries reads K_j
+      auto issue_s = [&](int x, int j, int b, bool last) {
+        uint64_t dq = dq0 + (uint64_t)((x * L::kTile) >> 4), dk = dk0 + slot16(pos_k(j));
+        const uint32_t t_s = tmem + col_s(b);
+        asm volatile("" : "+l"(dq), "+l"(dk));  // the sums below stay here: hoisted, they would not fit the registers
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * L::kAtomBytes + (kk & 3) * 32) >> 4);
-          mma_ss_e(n.s, n.dq + off, n.dk + off, id_s, kk > 0 ? 1u : 0u);
+          mma_ss_e(t_s, dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
         }
+        commit_e(bar_s(b));
+        if (last) commit_e(bar_empty(pos_k(j) % kSlots));
       };
-      auto commit_s = [&](int q) {
-        commit_e(bar_s(q % kS));
-        if (x_of(q) == 1 || nB == 0) commit_e(bar_empty(pos_k(j_of(q)) % kSlots));  // the last to read K_j
+      int b = 0;          // buffer and turn of the tile at hand
+      uint32_t turn = 0;
+      // One S tile of the sequence: O_x += P V_j, then S of (x2, j2), kS places on,
+      // into the same buffer.  The time from P to that S is on the path that bounds
+      // the kernel: what a half step waits for is asked for at once, and one vote
+      // settles it when everything is there already.
+      auto step = [&](auto x_, int j, bool first_v, bool last_v, bool more, int x2, int j2, bool first_k, bool last_k) {
+        constexpr int x = decltype(x_)::value;
+        const int pv = pos_v(j);
+        bool there = mbar_test_wait(bar_p(b, 0), turn);
+        if (first_v) there = there & slot_ready(pv);
+        uint64_t dv = dv0 + slot16(pv);
+        const uint32_t o = tmem + col_o(x), p = tmem + col_s(b);
+        asm volatile("" : "+l"(dv));
+        if (!__any_sync(0xffffffffu, there) &&
+            !((!first_v || wait_slot(pv)) && warp_spin_wait(bar_p(b, 0), turn, err, kErrWaitP, abort_flag)))
+          return false;
+        fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_e(o, p + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+        there = mbar_test_wait(bar_p(b, 1), turn);
+        if (more && first_k) there = there & slot_ready(pos_k(j2));
+        if (!__any_sync(0xffffffffu, there) && !((!more || !first_k || wait_slot(pos_k(j2))) &&
+                                                 warp_spin_wait(bar_p(b, 1), turn, err, kErrWaitP, abort_flag)))
+          return false;
+        fence_after_sync();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk) mma_ts_e(o, p + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id_o, 1u);
+        commit_e(bar_pv(x, j));  // before S's commit: who sees that S may count on this one
+        if (more) issue_s(x2, j2, b, last_k);
+        if (last_v) commit_e(bar_empty(pv % kSlots));
+        if (++b == kS) {
+          b = 0;
+          turn ^= 1;
+        }
+        return true;
       };
+      using A = std::integral_constant<int, 0>;
+      using Bt = std::integral_constant<int, 1>;
       const int nq = nA + nB;
       bool ok = true;
-      for (int q = 0; ok && q < min(kS, nq); ++q) {
-        if (!(ok = wait_slot(pos_k(j_of(q))) && warp_spin_wait(bar_q(x_of(q)), 0, err, kErrWaitLoad, abort_flag))) break;
-        fence_after_sync();
-        issue_s(next_s(q));
-        commit_s(q);
-      }
-      for (int q = 0; ok && q < nq; ++q) {
-        // all but P is waited for beforehand, tiles by their first reader only: the
-        // time from P to the next S is on the path that bounds the kernel
-        const int x = x_of(q), j = j_of(q), b = q % kS;
-        const bool more = q + kS < nq;
-        const Next n = next_s(more ? q + kS : q);
-        uint64_t dv = dv0 + slot16(pos_v(j));
-        const uint32_t o = tmem + col_o(x), p = tmem + col_s(b), turn = (q / kS) & 1;
-        asm volatile("" : "+l"(dv));
-        if ((x == 0 || j == nA) && !(ok = wait_slot(pos_v(j)))) break;
-        if (more && (x_of(q + kS) == 0 || j_of(q + kS) == nA) && !(ok = wait_slot(pos_k(j_of(q + kS))))) break;
-        // O_x += P V_j, each half of the keys once its P is there
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!(ok = warp_spin_wait(bar_p(b, half), turn, err, kErrWaitP, abort_flag))) break;
+      if (nB > 0) {  // A_0 B_0 A_1 B_1 ... B_nA
+        for (int q = 0; ok && q < min(kS, nq); ++q) {
+          const int x = q >= 2 * nA || (q & 1) ? 1 : 0, j = min(q >> 1, nA);
+          if (!(ok = wait_slot(pos_k(j)) && warp_spin_wait(bar_q(x), 0, err, kErrWaitLoad, abort_flag))) break;
           fence_after_sync();
-#pragma unroll
-          for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-            mma_ts_e(o, p + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+          issue_s(x, j, q, x == 1);
         }
-        if (!ok) break;
-        commit_e(bar_pv(x, j));  // before S's commit: who sees S(q + kS) may count on this one
-        if (more) {
-          issue_s(n);
-          commit_s(q + kS);
+        for (int j = 0; ok && j < nA; ++j) {
+          if (kS == 2) {
+            if (!(ok = step(A(), j, true, false, true, j + 1 < nA ? 0 : 1, j + 1, true, j + 1 == nA))) break;
+            ok = step(Bt(), j, false, true, j + 1 < nA, 1, j + 1, false, true);
+          } else {
+            if (!(ok = step(A(), j, true, false, j + 1 < nA, 1, j + 1, false, true))) break;
+            ok = step(Bt(), j, false, true, j + 2 <= nA, j + 2 < nA ? 0 : 1, j + 2, true, j + 2 == nA);
+          }
         }
-        if (x == 1 || nB == 0) commit_e(bar_empty(pos_v(j) % kSlots));
+        if (ok) ok = step(Bt(), nA, true, true, false, 1, 0, false, false);
+      } else {  // A alone
+        for (int j = 0; ok && j < min(kS, nA); ++j) {
+          if (!(ok = wait_slot(pos_k(j)) && warp_spin_wait(bar_q(0), 0, err, kErrWaitLoad, abort_flag))) break;
+          fence_after_sync();
+          issue_s(0, j, j, true);
+        }
+        for (int j = 0; ok && j < nA; ++j) ok = step(A(), j, true, true, j + kS < nA, 0, j + kS, true, true);
       }
       commit_e(bar_done);
       if (lane == 0) drain_wait(bar_done, 0, err);
