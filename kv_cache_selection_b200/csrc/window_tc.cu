@@ -26,7 +26,8 @@
 // the result overflows).
 //
 // Warps (384 threads): 0 TMA producer, 1 tensor-memory owner and MMA issuer,
-// 4..7 softmax of tile A, 8..11 of tile B.
+// 4..7 softmax of tile A, 8..11 of tile B.  The MMA warp shares its scheduler with a
+// warp of each softmax, so its waits suspend instead of polling.
 #include <type_traits>
 
 #include "common.cuh"
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv0 = sdesc_sw128(sb + L::kKV, L::kAtomBytes, 1024);
       auto slot16 = [&](int pos) { return (uint64_t)((pos % kSlots) * (L::kTile >> 4)); };
       auto wait_slot = [&](int pos) {
-        return warp_spin_wait(bar_full(pos % kSlots), (pos / kSlots) & 1, err, kErrWaitLoad, abort_flag);
+        return warp_wait_all(bar_full(pos % kSlots), (pos / kSlots) & 1, err, kErrWaitLoad, abort_flag);
       };
       auto slot_ready = [&](int pos) { return mbar_test_wait(bar_full(pos % kSlots), (pos / kSlots) & 1); };
       // S = Q_x K_j^T into buffer b; last: no other tile of queries reads K_j
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o = tmem + col_o(x), p = tmem + col_s(b);
         asm volatile("" : "+l"(dv));
         if (!__any_sync(0xffffffffu, there) &&
-            !((!first_v || wait_slot(pv)) && warp_spin_wait(bar_p(b, 0), turn, err, kErrWaitP, abort_flag)))
+            !((!first_v || wait_slot(pv)) && warp_wait_all(bar_p(b, 0), turn, err, kErrWaitP, abort_flag)))
           return false;
         fence_after_sync();
 #pragma unroll
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         there = mbar_test_wait(bar_p(b, 1), turn);
         if (more && first_k) there = there & slot_ready(pos_k(j2));
         if (!__any_sync(0xffffffffu, there) && !((!more || !first_k || wait_slot(pos_k(j2))) &&
-                                                 warp_spin_wait(bar_p(b, 1), turn, err, kErrWaitP, abort_flag)))
+                                                 warp_wait_all(bar_p(b, 1), turn, err, kErrWaitP, abort_flag)))
           return false;
         fence_after_sync();
 #pragma unroll
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nB > 0) {  // A_0 B_0 A_1 B_1 ... B_nA
         for (int q = 0; ok && q < min(kS, nq); ++q) {
           const int x = q >= 2 * nA || (q & 1) ? 1 : 0, j = min(q >> 1, nA);
-          if (!(ok = wait_slot(pos_k(j)) && warp_spin_wait(bar_q(x), 0, err, kErrWaitLoad, abort_flag))) break;
+          if (!(ok = wait_slot(pos_k(j)) && warp_wait_all(bar_q(x), 0, err, kErrWaitLoad, abort_flag))) break;
           fence_after_sync();
           issue_s(x, j, q, x == 1);
         }
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = step(Bt(), nA, true, true, false, 1, 0, false, false);
       } else {  // A alone
         for (int j = 0; ok && j < min(kS, nA); ++j) {
-          if (!(ok = wait_slot(pos_k(j)) && warp_spin_wait(bar_q(0), 0, err, kErrWaitLoad, abort_flag))) break;
+          if (!(ok = wait_slot(pos_k(j)) && warp_wait_all(bar_q(0), 0, err, kErrWaitLoad, abort_flag))) break;
           fence_after_sync();
           issue_s(0, j, j, true);
         }
