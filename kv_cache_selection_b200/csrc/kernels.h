@@ -125,9 +125,9 @@ cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspac
 cudaError_t launch_q4_attn_tc(const Q4AttnArgs& p, int d, cudaStream_t st);
 cudaError_t q4_attn_tc_status(int* code);
 
-// Causal attention of a sequence with a window (>= 1) and first tokens: float32 on
-// the CUDA cores, bf16 on the tensor cores, and the first error the latter's waits recorded.
-cudaError_t launch_window_simt(const WindowArgs& a, int d, cudaStream_t st);
+// Causal attention of a sequence with a window (>= 1) and first tokens: float32
+// (tf32 tensor cores), bf16 (tcgen05), and the first error the latter's waits recorded.
+cudaError_t launch_window_f32(const WindowArgs& a, int d, cudaStream_t st);
 cudaError_t launch_window_tc(const WindowArgs& a, int d, cudaStream_t st);
 cudaError_t window_tc_status(int* code);
 

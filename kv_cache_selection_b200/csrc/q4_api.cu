@@ -262,7 +262,7 @@ int sink_window_prefill_batched(const void* q, const void* k, const void* v, int
   a.n_sink = n_sink;
   a.scale_log2 = skv::kLog2e / sqrtf((float)d);
   const cudaError_t e = dtype == STATEKV_BF16 ? skv::launch_window_tc(a, d, static_cast<cudaStream_t>(stream))
-                                              : skv::launch_window_simt(a, d, static_cast<cudaStream_t>(stream));
+                                              : skv::launch_window_f32(a, d, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess)
     return fail(STATEKV_ERR_CUDA, "sink_window_prefill launch failed: %s", cudaGetErrorString(e));
   return STATEKV_OK;
