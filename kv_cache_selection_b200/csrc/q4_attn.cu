@@ -759,7 +759,12 @@ cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
 Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm) {
   Q4Plan pl{};
   const long long R = (long long)(Hq / Hkv) * n;
-  pl.rows = dtype == kDtypeF32 || R <= 8 ? 8 : R <= 16 ? 16 : 128;
+  // Measured in bf16 over 131072 tokens (4 KV heads, d = 128) and 32768 (2, d = 64),
+  // us: 12 rows as 8-row tiles 36.6, 10.3, as one of 16 rows 33.0, 11.2; 32 rows as
+  // 16-row tiles 53.2, 12.4, as one of 128 rows on tcgen05 52.0, 16.4 (whatever the
+  // rows, up to 128); more 16-row tiles each add some 20 us to the former.  float32
+  // takes two parts of everything, which fit the registers for eight rows only.
+  pl.rows = dtype == kDtypeF32 || R <= 8 ? 8 : R <= 32 ? 16 : 128;
   pl.n_rb = (int)((R + pl.rows - 1) / pl.rows);
   const long long sg = (long long)S * Hkv;
   size_t parts;
