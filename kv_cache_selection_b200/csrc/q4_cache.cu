@@ -4,6 +4,12 @@
 // head).  A V word holds codes of eight tokens, so a block that is only partly
 // covered by an append is read, merged and written by the one thread block that
 // owns it; no two thread blocks of a call share a word.
+//
+// Measured (B200, graph replays, 131072 tokens of 4 heads, d = 128, bf16, inputs
+// beyond L2): append 99 us (268 MB in, 75 MB out: 3.5 TB/s), bound by instructions
+// (82 % of the issue slots; the group ranges, exact ties and the packing), read 58
+// us (5.9 TB/s), bound by memory writes.  Sizes that no longer fill the SMs are bound by
+// latency: a 256-token frame appends in 8.3 us, a launch and four dependent passes.
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_cache.cuh"
@@ -255,7 +261,7 @@ __device__ __forceinline__ void transpose_nibbles(uint32_t (&a)[8]) {
 // Append.  A lane quantises sixteen channels of a token's key or value, D/16
 // lanes a token, with the next token's loads in flight (with eight channels a
 // lane the group's range and scale, which each of its lanes computes, cost as
-// much as the codes).  Eight channels of a key are one word of the block; values
+// much as the codes: 130 us where this takes 99).  Eight channels of a key are one word of the block; values
 // go through shared memory as nibbles, where a thread transposes eight tokens x
 // eight channels into V's words.  The block's image leaves as 16-byte stores.
 constexpr int kAppendThreads = 128;

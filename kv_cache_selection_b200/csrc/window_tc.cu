@@ -25,6 +25,14 @@
 // the CUDA cores (slow, and only where the inputs hold a NaN or an infinity or
 // the result overflows).
 //
+// Measured (B200): 65536 tokens, 28 heads, d = 128, window 4096: 3365 us, 1112
+// TFLOP/s; 4 x 4001 tokens, 14 heads, d = 64, window 1024: 130 us, 396 TFLOP/s.  At
+// d = 128 a pair of key tiles takes 3650 cycles for 2048 of products and 2048 of
+// exponentials: the bound is the chain S -> softmax (2180 cycles, half of them
+// exponentials) -> P V -> next S of each query tile, with two in flight.  At d = 64
+// (products of N = 64 cost as much as of N = 128) it is the scheduler that two
+// softmax warps share with the MMA warp.
+//
 // Warps (384 threads): 0 TMA producer, 1 tensor-memory owner and MMA issuer,
 // 4..7 softmax of tile A, 8..11 of tile B.  The MMA warp shares its scheduler with a
 // warp of each softmax, so its waits suspend instead of polling.
