@@ -694,3 +694,55 @@ def test_handle_decode_captured_in_a_graph():
     torch.cuda.synchronize()
     assert same(out, want)
     h.close()
+
+
+# ------------------------------------------------------------- longer sequences
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (100, 75)])
+def test_decode_of_many_text_tokens(window, n_sink, dtype):
+    """150 text tokens (300 rows of a KV head) after 70 cached ones: most of what a
+    row sees are text tokens."""
+    c, ins, out, lse, wants = run_decode(2, 4, 2, 64, 70, 150, window, n_sink, dtype)
+    for s in range(2):
+        check_attention(out[s], lse[s], wants[s], dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
+
+
+@cuda
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (64, "f32"), (128, "f32")])
+def test_sink_window_prefill_gives_the_same_bits_again(d, dtype):
+    """Enough blocks for every order of arrival: ten runs, one result."""
+    k, v = tokens(1, 2, 2500, 2, d, dtype)
+    q, _ = tokens(2, 2, 2500, 14, d, dtype, loud=False)
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    first = _skv().sink_window_prefill(q, k, v, 300, n_sink=4)
+    for _ in range(9):
+        again = _skv().sink_window_prefill(q, k, v, 300, n_sink=4)
+        assert same(first[0], again[0]) and same(first[1], again[1])
+    assert _skv().sink_window_status() == 0
+
+
+@cuda
+@pytest.mark.parametrize("d", [64, 128])
+def test_sink_window_prefill_f32_of_the_largest_values(d):
+    """float32 values that no rounding up survives: 3.4e38 in a value (rows that see
+    it are huge in one channel, the others untouched) and in a key that meets tiny
+    queries (one dominant logit of 4e7), both inside and outside the window."""
+    n, window, top = 300, 70, 3.4028e38
+    k, v = tokens(1, 1, n, 1, d, "f32")
+    q, _ = tokens(2, 1, n, 2, d, "f32", loud=False)
+    clean = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)[0].cpu()
+    v[0, 100, 0, 5] = top
+    v[0, 131, 0, 9] = -top
+    out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)
+    check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, window, 2), "f32", 0.0)
+    assert same(out[:, :100].cpu(), clean[:, :100]) and same(out[:, 131 + window:].cpu(), clean[:, 131 + window:])
+    k[0, 60, 0, 7] = top
+    q[0, 40:90] *= 1e-30
+    q[0, 40:90, :, 7] = 1e-30
+    out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)
+    w = reference(q[0], k[0], v[0], None, None, window, 2)
+    rows = slice(0, 90)                    # the rows behind it meet 3.4e38 with queries of size 1
+    part = Want((w[0][rows], w[1][:, rows], w[2][rows], w[3][:, rows]))
+    part.keys = w.keys
+    check_attention(out[0, rows], lse[0][:, rows], part, "f32", 0.0)
