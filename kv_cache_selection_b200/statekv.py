@@ -92,7 +92,13 @@ def _check(rc, handle=None):
         raise StateKVError(rc, msg.decode() if msg else "")
 
 
+_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
 def _dtype_code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is not None:
+        return code
     if dtype in ("bf16", torch.bfloat16, BF16):
         return BF16
     if dtype in ("f32", torch.float32, F32):
@@ -104,6 +110,10 @@ def _torch_dtype(code: int):
     return torch.bfloat16 if code == BF16 else torch.float32
 
 
+# the current device and whether its current stream is capturing, without the
+# wrappers' own checks (CUDA is up: the callers hold tensors on it)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 # the current stream's handle without building a torch.cuda.Stream object
 _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -350,7 +360,7 @@ def full_causal_prefill(q, k, v, out=None, lse=None, with_lse=True, stream=None)
 def _on(dev):
     """Makes a tensor's device the current one; returns the device to go back
     to, or -1 where it already was."""
-    now = torch.cuda.current_device()
+    now = _current_device()
     if now == dev:
         return -1
     torch.cuda.set_device(dev)
@@ -413,8 +423,8 @@ class Q4Cache:
         shape = t.shape
         if n is None:
             n = shape[-3] if len(shape) >= 3 else 0
-        if not (t.get_device() == self._dev >= 0 and t.dtype is dtype and t.is_contiguous()
-                and (shape == (self.S, n, heads, self.d) or (self.S == 1 and shape == (n, heads, self.d)))):
+        if not (t.is_cuda and t.dtype is dtype and (shape == (self.S, n, heads, self.d) or (self.S == 1 and shape == (n, heads, self.d)))
+                and t.is_contiguous() and t.get_device() == self._dev):
             lead = (self.S,) if t.dim() == 4 or self.S != 1 else ()
             _need(t, lead + (n, heads, self.d), dtype, name)
             raise ValueError(f"{name} is on {t.device}, the cache on {self.data.device}")
@@ -497,7 +507,8 @@ class Q4Cache:
         if with_lse or lse is not None:
             ls = (self.S, Hq, n) if len(shape) == 4 else (Hq, n)
             if lse is None:
-                lse = _empty(self._proto[torch.float32], ls, stream)
+                proto = self._proto[torch.float32]
+                lse = proto.new_empty(ls) if stream is None else _empty(proto, ls, stream)
             else:
                 self._need_like(lse, ls, torch.float32, "lse")
         back = _on(self._dev)
@@ -511,7 +522,7 @@ class Q4Cache:
             st = _stream_ptr(stream, self._dev)
             args = (self._ptr, self.S, Hq, self.Hkv, self.d, self.capacity, q.data_ptr(), k.data_ptr(), v.data_ptr(), n,
                     code, host, dev, window, n_sink, out.data_ptr(), lse.data_ptr() if lse is not None else None)
-            if stream is not None or torch.cuda.is_current_stream_capturing():
+            if stream is not None or _capturing():
                 # a workspace of the call's own: the stream may be anybody's, and
                 # a captured graph keeps its memory to itself
                 ws = _empty(self._proto[torch.bfloat16], (need // 2,), stream)
