@@ -119,6 +119,7 @@ struct Q4Plan {
   size_t o_bytes, bytes;
 };
 Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm);
+bool q4_alone(const WindowArgs& a, const Q4Plan& pl);  // one launch instead of two (no merge)
 cudaError_t q4_attn_status(int* code);  // first error its waits recorded
 cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st);
 // Its kernel for 128-row tiles (tensor cores), and the first error its waits recorded.

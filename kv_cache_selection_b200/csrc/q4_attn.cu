@@ -63,6 +63,13 @@ constexpr float kRaise = 6.f;   // log2 headroom of the lazy row maximum
 constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
 constexpr float kPScale = 512.f;    // P s <= 2^6 * 512 < 65504
 
+// Short caches: one thread block per (stream, KV head, row tile) takes all of its
+// blocks, two a warp, joins the text tokens and writes the results: no partials, no
+// second launch.  One token, 4 KV heads, d = 128: 32 cached tokens 5.7 us against
+// 6.8 shared out and merged, 300 6.6 against 7.2, 1024 8.8 against 7.9 (32 pairs of
+// stream and head: 9.4 against 11.6); a launch less is 2.7 us of the host's time.
+constexpr int kAloneBlocks = 24, kAloneText = 32;
+
 __device__ int g_err;  // first error of the ring's waits of all calls on a device
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -161,7 +168,51 @@ __device__ __forceinline__ Deal deal_of(const WindowArgs& a, int W) {
   return d;
 }
 
-template <typename T, int D, int NT, int NS>
+// A row's running maximum (log2), sum and accumulator, in a warp: E channels a lane.
+template <int E>
+struct RowSum {
+  float m = -INFINITY, l = 0.f, acc[E];
+  __device__ __forceinline__ RowSum() {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  }
+  __device__ __forceinline__ void join(float m2, float l2, const float (&v)[E]) {  // acc += v (weights relative to 2^m2)
+    const float nm = fmaxf(m, m2);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    const float f1 = tc::ex2_approx(m - ref), f2 = tc::ex2_approx(m2 - ref);
+    l = l * f1 + l2 * f2;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + v[e] * f2;
+    m = nm;
+  }
+};
+// The text tokens first, first + step, ... that the row (text token i, head h) sees.
+template <typename T, int D>
+__device__ __forceinline__ void join_text(const WindowArgs& a, int L, int s, int h, int g, int i, int first, int step,
+                                          RowSum<D / 32>& sum) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+  float qv[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) qv[e] = to_f(q[e]) * a.scale_log2;
+  for (int j = first; j <= i; j += step) {
+    if (a.window && j <= i - a.window && (long long)L + j >= a.n_sink) continue;
+    const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
+    float t = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      t = fmaf(qv[e], to_f(static_cast<const T*>(a.k)[at + e]), t);
+      v[e] = to_f(static_cast<const T*>(a.v)[at + e]);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    if (t != t) sum.l = t;  // a NaN logit makes the row NaN
+    sum.join(t, 1.f, v);
+  }
+}
+
+template <typename T, int D, int NT, int NS, bool kAlone>
 __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   using B = Q4Block<D>;
   constexpr int kWarps = warps_of<NT, NS>();
@@ -197,22 +248,28 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 
   pdl_wait();
   pdl_trigger();
-  const Deal deal = deal_of(a, p.W);
-  if ((int)blockIdx.x >= deal.W) return;
-  int x = deal.first(blockIdx.x);
-  const int x_end = deal.first(blockIdx.x + 1);
-  int s = 0, s_base = 0;
-  Visible vis = visible_of(a, 0);
+  int x = 0, x_end = 1, s = kAlone ? blockIdx.x / a.Hkv : 0, s_base = 0;
+  if (!kAlone) {
+    const Deal deal = deal_of(a, p.W);
+    if ((int)blockIdx.x >= deal.W) return;
+    x = deal.first(blockIdx.x);
+    x_end = deal.first(blockIdx.x + 1);
+  }
+  Visible vis = visible_of(a, s);
   // text tokens of the tile's rows (rows behind R take the last one)
   const int i_first = row0 / G, i_last = (min(row0 + kRows, R) - 1) / G;
 
   while (x < x_end) {
-    while (x >= s_base + a.Hkv * vis.count()) {
-      s_base += a.Hkv * vis.count();
-      vis = visible_of(a, ++s);
+    int g = blockIdx.x % a.Hkv, v0 = 0, v1 = vis.count();
+    if (!kAlone) {
+      while (x >= s_base + a.Hkv * vis.count()) {
+        s_base += a.Hkv * vis.count();
+        vis = visible_of(a, ++s);
+      }
+      g = (x - s_base) / vis.count();
+      v0 = (x - s_base) - g * vis.count();
+      v1 = min(vis.count(), v0 + (x_end - x));
     }
-    const int g = (x - s_base) / vis.count(), v0 = (x - s_base) - g * vis.count();
-    const int v1 = min(vis.count(), v0 + (x_end - x));
     const uint8_t* base = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
 
     // Q's loads go out before the ring's, which would be ahead of them in every
@@ -575,6 +632,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     __syncthreads();
     float* wo = reinterpret_cast<float*>(smem);                        // [kWarps][kRows][kStride]
     float* wml = wo + kWarps * kRows * kStride;                        // [kWarps][kRows][2]
+    float* row_ml = wml + kWarps * kRows * 2;                          // [kRows][2]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -619,8 +677,27 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
         acc.z += f * x4.z;
         acc.w += f * x4.w;
       }
-      *reinterpret_cast<float4*>(p.part_o + (part * kRows + r) * D + c * 4) = acc;
-      if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (part * kRows + r) * 2) = make_float2(mx, ls);
+      // alone: over the first warp's row, which no other thread reads here
+      *reinterpret_cast<float4*>(kAlone ? wo + r * kStride + c * 4 : p.part_o + (part * kRows + r) * D + c * 4) = acc;
+      if (c == 0) *reinterpret_cast<float2*>(kAlone ? row_ml + r * 2 : p.part_ml + (part * kRows + r) * 2) = make_float2(mx, ls);
+    }
+    if (kAlone) {  // a warp per row: its sum, then the text tokens
+      __syncthreads();
+      constexpr int E = D / 32;
+      for (int r = warp; r < min(kRows, R - row0); r += kWarps) {
+        const int i = (row0 + r) / G, h = g * G + (row0 + r) % G;
+        RowSum<E> sum;
+        sum.m = row_ml[r * 2];
+        sum.l = row_ml[r * 2 + 1];
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum.acc[e] = wo[r * kStride + lane * E + e];
+        join_text<T, D>(a, vis.L, s, h, g, i, 0, 1, sum);
+        T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = from_f<T>(sum.acc[e] / sum.l);
+        if (lane == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (sum.m + log2f(sum.l)) * kLn2;
+      }
+      return;
     }
     // the next segment's copies come over what was written here
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -644,37 +721,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
   const long long rw = blockIdx.x;
   const int i = (int)(rw % a.n), h = (int)(rw / a.n % a.Hq), s = (int)(rw / a.n / a.Hq);
   const int g = h / G, row = i * G + h % G;
-  float acc[E], m = -INFINITY, l = 0.f, qv[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  auto join = [&](float m2, float l2, const float (&v)[E]) {  // acc += v (weights relative to 2^m2)
-    const float nm = fmaxf(m, m2);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    const float f1 = tc::ex2_approx(m - ref), f2 = tc::ex2_approx(m2 - ref);
-    l = l * f1 + l2 * f2;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + v[e] * f2;
-    m = nm;
-  };
+  RowSum<E> sum;
   // the call's own tokens (inputs of the call: read before the wait)
   const Visible vis = visible_of(a, s);
-  const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = to_f(q[e]) * a.scale_log2;
-  for (int j = warp; j <= i; j += kMergeWarps) {
-    if (a.window && j <= i - a.window && (long long)vis.L + j >= a.n_sink) continue;
-    const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
-    float t = 0.f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      t = fmaf(qv[e], to_f(static_cast<const T*>(a.k)[at + e]), t);
-      v[e] = to_f(static_cast<const T*>(a.v)[at + e]);
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    if (t != t) l = t;  // a NaN logit makes the row NaN
-    join(t, 1.f, v);
-  }
+  join_text<T, D>(a, vis.L, s, h, g, i, warp, kMergeWarps, sum);
   // where the partials are
   int w0 = 0, w1 = -1, r = 0;
   long long part0 = 0;
@@ -716,29 +766,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b)
-        if (w + b * kMergeWarps <= w1) join(ml[b].x, ml[b].y, v[b]);
+        if (w + b * kMergeWarps <= w1) sum.join(ml[b].x, ml[b].y, v[b]);
     }
   }
   if (lane == 0) {
-    s_ml[warp][0] = m;
-    s_ml[warp][1] = l;
+    s_ml[warp][0] = sum.m;
+    s_ml[warp][1] = sum.l;
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = sum.acc[e];
   __syncthreads();
   float mx = -INFINITY;
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, s_ml[w][0]);
   const float ref = mx == -INFINITY ? 0.f : mx;
   for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) {
-    float sum = 0.f, ls = 0.f;
+    float o = 0.f, ls = 0.f;
 #pragma unroll
     for (int w = 0; w < kMergeWarps; ++w) {
       const float f = tc::ex2_approx(s_ml[w][0] - ref);
       ls += f * s_ml[w][1];
-      sum += f * s_acc[w][d];
+      o += f * s_acc[w][d];
     }
-    static_cast<T*>(a.out)[(((long long)s * a.n + i) * a.Hq + h) * D + d] = from_f<T>(sum / ls);
+    static_cast<T*>(a.out)[(((long long)s * a.n + i) * a.Hq + h) * D + d] = from_f<T>(o / ls);
     if (d == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (mx + log2f(ls)) * kLn2;
   }
 }
@@ -749,17 +799,29 @@ cudaError_t launch_merge(const Q4AttnArgs& p, cudaStream_t st) {
   return launch_kernel(q4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(kMergeWarps * 32), 0, st, true, p);
 }
 
-template <typename T, int D, int NT, int NS>
-cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
+template <typename T, int D, int NT, int NS, bool kAlone>
+cudaError_t launch_as(const Q4AttnArgs& p, unsigned workers, cudaStream_t st) {
   using B = Q4Block<D>;
   constexpr int kWarps = warps_of<NT, NS>();
   constexpr int ring = kWarps * kStages * B::kBytes;
-  constexpr int merge = kWarps * 8 * NT * (D + 4 + 2) * 4;
+  constexpr int merge = (kWarps * (D + 4 + 2) + 2) * 8 * NT * 4;
   constexpr int smem = ring > merge ? ring : merge;
-  cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS>, smem);
+  const cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS, kAlone>, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(q4_attn_kernel<T, D, NT, NS>, dim3(p.W, p.n_rb), dim3(kWarps * 32), smem, st, false, p);
+  return launch_kernel(q4_attn_kernel<T, D, NT, NS, kAlone>, dim3(workers, p.n_rb), dim3(kWarps * 32), smem, st, false, p);
+}
+template <typename T, int D, int NT, int NS>
+cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
+  if (p.W == 0) return launch_as<T, D, NT, NS, true>(p, p.w.S * p.w.Hkv, st);
+  const cudaError_t e = launch_as<T, D, NT, NS, false>(p, p.W, st);
   return e != cudaSuccess ? e : launch_merge<T, D>(p, st);
+}
+
+// Blocks that can be visible in a stream, by what the host knows.
+long long most_blocks(const WindowArgs& a) {
+  const long long len = a.lengths ? a.capacity : a.length, all = (len + 31) / 32;
+  if (!a.window) return all;
+  return std::min(all, (std::min<long long>(a.n_sink, len) + 31) / 32 + (a.window + 31ll) / 32 + 1);
 }
 
 }  // namespace
@@ -788,6 +850,10 @@ Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm) {
   return pl;
 }
 
+bool q4_alone(const WindowArgs& a, const Q4Plan& pl) {
+  return pl.rows != 128 && most_blocks(a) <= kAloneBlocks && a.n <= kAloneText && (long long)a.S * a.Hkv <= pl.W;
+}
+
 cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st) {
   Q4AttnArgs p{};
   p.w = a;
@@ -796,14 +862,12 @@ cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspac
   p.n_rb = pl.n_rb;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.o_bytes);
+  if (q4_alone(a, pl)) p.W = 0;
   if (dtype == kDtypeF32) return d == 128 ? launch<float, 128, 1, 2>(p, st) : launch<float, 64, 1, 2>(p, st);
   if (pl.rows == 8) return d == 128 ? launch<__nv_bfloat16, 128, 1, 1>(p, st) : launch<__nv_bfloat16, 64, 1, 1>(p, st);
   if (pl.rows == 16) return d == 128 ? launch<__nv_bfloat16, 128, 2, 1>(p, st) : launch<__nv_bfloat16, 64, 2, 1>(p, st);
   // no more splits than 128-token tiles can be visible
-  const long long len = a.lengths ? a.capacity : a.length;
-  long long blocks = (len + 31) / 32;
-  if (a.window) blocks = std::min(blocks, (std::min<long long>(a.n_sink, len) + 31) / 32 + (a.window + 31ll) / 32 + 1);
-  p.W = (int)std::max(1ll, std::min((long long)p.W, (blocks + 3) / 4));
+  p.W = (int)std::max(1ll, std::min((long long)p.W, (most_blocks(a) + 3) / 4));
   const cudaError_t e = launch_q4_attn_tc(p, d, st);
   if (e != cudaSuccess) return e;
   return d == 128 ? launch_merge<__nv_bfloat16, 128>(p, st) : launch_merge<__nv_bfloat16, 64>(p, st);

@@ -817,7 +817,12 @@ int statekv_decode(statekv_t h, int layer, const void* q, const void* k, const v
                                      lse, h->dec_ws, need, stream);
     sc.done();
     if (rc) return set_err(h, rc, "%s", std::string(g_free_error).c_str());
-    ++h->launches;  // the merge
+    skv::WindowArgs wa{};
+    wa.S = S;
+    wa.Hkv = Hkv;
+    wa.n = n_text;
+    wa.length = N;
+    if (!skv::q4_alone(wa, skv::q4_plan(S, Hq, Hkv, n_text, h->dtype, d, h->n_sm))) ++h->launches;  // the merge
     return STATEKV_OK;
   }
   if (h->dtype != STATEKV_BF16) {

@@ -643,6 +643,7 @@ def test_handle_decode_before_any_frame_and_format_refusals():
     q, k, v, _ = (t.cuda() for t in frame(1, 1, 16, 6, 2, 64, "bf16"))
     a, b = (h.decode(0, q[:2].contiguous(), k[:2].contiguous(), v[:2].contiguous()) for h in (native, q4))
     assert q4.get_detailed(0)["len"] == 0
+    assert q4.kernel_launches() == 1          # nothing to share out, nothing to merge
     want = reference(q[:2].cpu(), k[:2].cpu(), v[:2].cpu(), None, None, 0, 0)
     check_attention(b[0], b[1], want, "bf16", 2.0 ** -11)
     check_attention(a[0], a[1], want, "bf16", 2.0 ** -8)
@@ -672,7 +673,9 @@ def test_handle_decode_captured_in_a_graph():
     q, k, v, _ = (t.cuda() for t in frame(9, S, T, Hq, Hkv, d, "bf16"))
     one = [t[:1].clone() for t in (q, k, v)]
     many = [t.contiguous() for t in (q, k, v)]
+    before = h.kernel_launches()
     want = h.decode(0, *one)[0].clone()
+    assert h.kernel_launches() == before + 1  # 150 tokens: a block per KV head
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     g = torch.cuda.CUDAGraph()
@@ -686,7 +689,9 @@ def test_handle_decode_captured_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert same(out, want)
+    before = h.kernel_launches()
     h.decode(0, *many)                  # grows the scratch
+    assert h.kernel_launches() == before + 2  # 150 rows of a KV head: splits and their merge
     one[0].mul_(2)
     want = h.decode(0, *one)[0].clone()
     torch.cuda.synchronize()
@@ -746,3 +751,25 @@ def test_sink_window_prefill_f32_of_the_largest_values(d):
     part = Want((w[0][rows], w[1][:, rows], w[2][rows], w[3][:, rows]))
     part.keys = w.keys
     check_attention(out[0, rows], lse[0][:, rows], part, "f32", 0.0)
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,window,n_sink", [(1, 0, 0), (3, 0, 0), (3, 90, 5)])
+def test_decode_is_the_same_on_either_side_of_a_kernel_border(n, window, n_sink, dtype):
+    """768 cached tokens (one block per KV head), 769 (shared out and merged) and, in
+    a cache whose lengths only the device knows, both."""
+    S, Hq, Hkv, d = 2, 8, 2, 64
+    pk, pv = tokens(1, S, 800, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    ins = [t.cuda() for t in (q, k, v)]
+    c = _skv().Q4Cache(Hkv, d, 800, n_streams=S)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    hk, hv = O.q4_held(pk), O.q4_held(pv)
+    lens = torch.tensor([768, 0], dtype=torch.int32, device="cuda")
+    for at, of in ((768, [768] * 2), (769, [769] * 2), (lens, [768, 0])):
+        out, lse = c.decode(*ins, at, window=window, n_sink=n_sink)
+        for s in range(S):
+            want = reference(q[s], k[s], v[s], hk[s, :of[s]], hv[s, :of[s]], window, n_sink)
+            check_attention(out[s], lse[s], want, dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
