@@ -552,27 +552,34 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
     """Causal attention with a sliding window and n_sink first tokens that stay
     visible, over q [(S,) N, Hq, d], k/v [(S,) N, Hkv, d]: token i sees j <= i
     with j > i - window or j < n_sink.  Returns (out, lse [(S,) Hq, N] or None)."""
-    batched = q.dim() == 4
-    S = q.shape[0] if batched else 1
-    N, Hq, d = q.shape[-3:]
-    Hkv = k.shape[-2]
-    code = _dtype_code(q.dtype)
-    lead = (S,) if batched else ()
-    _need(q, lead + (N, Hq, d), q.dtype, "q")
-    _need(k, lead + (N, Hkv, d), q.dtype, "k")
-    _need(v, lead + (N, Hkv, d), q.dtype, "v")
-    if out is None:
-        out = _empty(q, q.shape, stream)
-    else:
-        _need(out, lead + (N, Hq, d), q.dtype, "out")
-    if lse is None and with_lse:
-        lse = _empty(q if q.dtype is torch.float32 else _float32_on(q.device), lead + (Hq, N), stream)
-    elif lse is not None:
-        _need(lse, lead + (Hq, N), torch.float32, "lse")
+    shape, kshape, dt = q.shape, k.shape, q.dtype
+    lead = (shape[0],) if len(shape) == 4 else ()
+    S = shape[0] if lead else 1
+    N, Hq, d = shape[-3:]
+    Hkv = kshape[-2]
+    code = _dtype_code(dt)
     dev = q.get_device()
-    for t, name in ((k, "k"), (v, "v"), (out, "out"), (lse, "lse")):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    if not (q.is_cuda and q.is_contiguous() and kshape == lead + (N, Hkv, d) and v.shape == kshape and k.dtype is dt
+            and v.dtype is dt and k.is_contiguous() and v.is_contiguous() and k.get_device() == dev == v.get_device()):
+        _need(q, lead + (N, Hq, d), dt, "q")
+        for t, name in ((k, "k"), (v, "v")):
+            _need(t, lead + (N, Hkv, d), dt, name)
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    mine = out is None, lse is None
+    if out is None:
+        out = torch.empty_like(q) if stream is None else _empty(q, shape, stream)
+    if lse is None and with_lse:
+        proto = q if dt is torch.float32 else _float32_on(q.device)
+        lse = proto.new_empty(lead + (Hq, N)) if stream is None else _empty(proto, lead + (Hq, N), stream)
+    if mine != (True, True):
+        for t, own, want, wdt, name in ((out, mine[0], lead + (N, Hq, d), dt, "out"),
+                                        (lse, mine[1], lead + (Hq, N), torch.float32, "lse")):
+            if own:
+                continue
+            _need(t, want, wdt, name)
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
     back = _on(dev)
     try:
         rc = lib.sink_window_prefill_batched(q.data_ptr(), k.data_ptr(), v.data_ptr(), S, N, Hq, Hkv, d, code, window,
