@@ -6,9 +6,10 @@
 //   x y ~ lo_x hi_y + hi_x lo_y + hi_x hi_y,
 // off by 2^-21 of |x y| at most, with signs that do not add up.  mma.sync's tf32
 // rate bounds the kernel: 146 TFLOP/s, 49 of the result (4 x 3000 tokens, 16
-// heads, d = 64).  The same tiles on the CUDA cores (paired fma) reached 34, three
-// bfloat16 parts and six products at the 16-bit rate 41 (their splitting, by every
-// warp, takes more instructions than the products).  Sums are float32; the tensor
+// heads, d = 64).  The same tiles on the CUDA cores (paired fma) reached 34; three
+// bfloat16 parts and six products at the 16-bit rate 42, split by every warp or
+// once a block (chains of six dependent products, and registers for two warps a
+// scheduler).  Sums are float32; the tensor
 // cores cut theirs instead of rounding, so each 16 channels of S and each key
 // tile of P V are summed on their own and added on the CUDA cores: 3.0e-7 off in
 // all (1500 tokens, d = 128) where one long sum was 1.2e-6 off.
