@@ -23,6 +23,11 @@
 //     an eighth of what the bf16 result rounds by; float32 again takes two parts.
 //   P: relative to a row maximum that moves only when a logit exceeds it by
 //     more than 2^6, so that most blocks need one vote and no shuffle.
+// The tensor cores cut their float32 sums instead of rounding them, which a long
+// sum adds up: in float32 calls eight channels of S and each block's P V are summed
+// on their own, least parts first, and added on the CUDA cores (6.8e-7 off over
+// 32768 tokens, d = 128, where running sums were 4.6e-6 off; as fast).  A bf16 result
+// does not see it.
 // Tensor-core shape m16n8k16 with tokens (K) or channels (V) as the 16 rows and
 // query rows as the 8 columns: the fragments come from shared memory as stored,
 // S^T turns into P^T's fragment by an 8x8 transpose, and nothing but 4-bit codes
@@ -413,15 +418,24 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
           codes_of<kCentred>(ka[w], fa);
           codes_of<kCentred>(kb[w], fb);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            float (&c)[4] = acc[nt][w >> 1];
+            if (kCentred) {
+              float part[4];
+              mma16816_first(part, fa[0], fb[0], fa[1], fb[1], qf[nt][NS - 1][2 * w][0], qf[nt][NS - 1][2 * w][1]);
+              mma16816(part, fa[2], fb[2], fa[3], fb[3], qf[nt][NS - 1][2 * w + 1][0], qf[nt][NS - 1][2 * w + 1][1]);
+              mma16816(part, fa[0], fb[0], fa[1], fb[1], qf[nt][0][2 * w][0], qf[nt][0][2 * w][1]);
+              mma16816(part, fa[2], fb[2], fa[3], fb[3], qf[nt][0][2 * w + 1][0], qf[nt][0][2 * w + 1][1]);
 #pragma unroll
-            for (int ns = 0; ns < NS; ++ns) {
-              if ((w & 1) == 0 && ns == 0)
-                mma16816_first(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
+              for (int e = 0; e < 4; ++e) c[e] = (w & 1) == 0 ? part[e] : c[e] + part[e];
+            } else {
+              if ((w & 1) == 0)
+                mma16816_first(c, fa[0], fb[0], fa[1], fb[1], qf[nt][0][2 * w][0], qf[nt][0][2 * w][1]);
               else
-                mma16816(acc[nt][w >> 1], fa[0], fb[0], fa[1], fb[1], qf[nt][ns][2 * w][0], qf[nt][ns][2 * w][1]);
-              mma16816(acc[nt][w >> 1], fa[2], fb[2], fa[3], fb[3], qf[nt][ns][2 * w + 1][0], qf[nt][ns][2 * w + 1][1]);
+                mma16816(c, fa[0], fb[0], fa[1], fb[1], qf[nt][0][2 * w][0], qf[nt][0][2 * w][1]);
+              mma16816(c, fa[2], fb[2], fa[3], fb[3], qf[nt][0][2 * w + 1][0], qf[nt][0][2 * w + 1][1]);
             }
+          }
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -607,12 +621,20 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
           codes_of<kCentred>(x0, fa);
           codes_of<kCentred>(x1, fb);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            if (kCentred) {
+              float acc[4];
+              mma16816_first(acc, fa[0], fb[0], fa[1], fb[1], pf[nt][NS - 1][gg][0][0], pf[nt][NS - 1][gg][0][1]);
+              mma16816(acc, fa[2], fb[2], fa[3], fb[3], pf[nt][NS - 1][gg][1][0], pf[nt][NS - 1][gg][1][1]);
+              mma16816(acc, fa[0], fb[0], fa[1], fb[1], pf[nt][0][gg][0][0], pf[nt][0][gg][0][1]);
+              mma16816(acc, fa[2], fb[2], fa[3], fb[3], pf[nt][0][gg][1][0], pf[nt][0][gg][1][1]);
 #pragma unroll
-            for (int ns = 0; ns < NS; ++ns) {
-              mma16816(o[nt][2 * c + half], fa[0], fb[0], fa[1], fb[1], pf[nt][ns][gg][0][0], pf[nt][ns][gg][0][1]);
-              mma16816(o[nt][2 * c + half], fa[2], fb[2], fa[3], fb[3], pf[nt][ns][gg][1][0], pf[nt][ns][gg][1][1]);
+              for (int e = 0; e < 4; ++e) o[nt][2 * c + half][e] += acc[e];
+            } else {
+              mma16816(o[nt][2 * c + half], fa[0], fb[0], fa[1], fb[1], pf[nt][0][gg][0][0], pf[nt][0][gg][0][1]);
+              mma16816(o[nt][2 * c + half], fa[2], fb[2], fa[3], fb[3], pf[nt][0][gg][1][0], pf[nt][0][gg][1][1]);
             }
+          }
         }
       }
       __syncwarp();

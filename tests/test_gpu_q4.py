@@ -773,3 +773,27 @@ def test_decode_is_the_same_on_either_side_of_a_kernel_border(n, window, n_sink,
         for s in range(S):
             want = reference(q[s], k[s], v[s], hk[s, :of[s]], hv[s, :of[s]], window, n_sink)
             check_attention(out[s], lse[s], want, dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
+
+
+@cuda
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_f32_of_a_long_cache_keeps_its_precision(d):
+    """Long float32 sums: the weights are off by 2^-22 (the exponential), 2^-22 (two
+    fp16 parts) and 2^-21 (the roundings of a logit of size 8) at most, 2^-20
+    together, independent of the values they meet, so the result is off by no more
+    relative to its norm; twice that leaves room for the sums over the blocks.  A
+    bias of the sums would show as a multiple of it."""
+    S, Hq, Hkv, L, n = 2, 14, 2, 32768, 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn((S, L, Hkv, d), generator=g, device="cuda") for _ in range(2))
+    q = torch.randn((S, n, Hq, d), generator=g, device="cuda")
+    c = _skv().Q4Cache(Hkv, d, L, n_streams=S)
+    c.append(k, v, 0)
+    tk, tv = (torch.randn((S, n, Hkv, d), generator=g, device="cuda") for _ in range(2))
+    out, _ = c.decode(q, tk, tv, L)
+    hk, hv = c.read(0, L, dtype="f32")
+    K, V = (torch.cat([x, y], 1).double().repeat_interleave(Hq // Hkv, 2) for x, y in ((hk, tk), (hv, tv)))
+    w = torch.softmax(torch.einsum("sihd,sjhd->shij", q.double(), K) / d ** 0.5, -1)
+    want = torch.einsum("shij,sjhd->sihd", w, V)
+    rel = ((out.double() - want).norm() / want.norm()).item()
+    assert rel <= 2.0 ** -19, f"{rel:.3g}"
