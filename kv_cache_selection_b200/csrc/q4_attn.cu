@@ -68,12 +68,7 @@ constexpr float kRaise = 6.f;   // log2 headroom of the lazy row maximum
 constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
 constexpr float kPScale = 512.f;    // P s <= 2^6 * 512 < 65504
 
-// Short caches: one thread block per (stream, KV head, row tile) takes all of its
-// blocks, two a warp, joins the text tokens and writes the results: no partials, no
-// second launch.  One token, 4 KV heads, d = 128: 32 cached tokens 5.7 us against
-// 6.8 shared out and merged, 300 6.6 against 7.2, 1024 8.8 against 7.9 (32 pairs of
-// stream and head: 9.4 against 11.6); a launch less is 2.7 us of the host's time.
-constexpr int kAloneBlocks = 24, kAloneText = 32;
+constexpr int kOwnText = 32;  // most text tokens of a call whose thread blocks join them one by one
 
 __device__ int g_err;  // first error of the ring's waits of all calls on a device
 
@@ -158,15 +153,46 @@ struct Deal {
     return x < head ? x / (q + 1) : r + (x - head) / q;
   }
 };
+// Visible blocks of a KV head in the streams before `end` (a whole warp calls it:
+// lengths on the device are summed by its lanes).
+template <bool kRagged>
+__device__ __forceinline__ int blocks_before(const WindowArgs& a, int end) {
+  if (!kRagged) return end * visible_of(a, 0).count();
+  int sum = 0;
+  for (int s = threadIdx.x & 31; s < end; s += 32) sum += visible_of(a, s).count();
+  return __reduce_add_sync(0xffffffffu, sum);
+}
+// The stream of block number x (below the total), and the number of its first block.
+template <bool kRagged>
+__device__ __forceinline__ int stream_of(const WindowArgs& a, int x, int& first) {
+  if (!kRagged) {
+    const int each = visible_of(a, 0).count() * a.Hkv, s = x / each;
+    first = s * each;
+    return s;
+  }
+  const int lane = threadIdx.x & 31;
+  first = 0;
+  for (int s0 = 0;; s0 += 32) {
+    const int mine = s0 + lane < a.S ? visible_of(a, s0 + lane).count() * a.Hkv : 0;
+    int upto = mine;  // of streams s0 .. s0 + lane
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, first + upto > x);
+    if (past || s0 + 32 >= a.S) {  // (always found for x below the total)
+      const int at = past ? __ffs(past) - 1 : 31;
+      first += __shfl_sync(0xffffffffu, upto - mine, at);
+      return min(s0 + at, a.S - 1);
+    }
+    first += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+template <bool kRagged>
 __device__ __forceinline__ Deal deal_of(const WindowArgs& a, int W) {
   Deal d;
-  d.total = 0;
-  if (a.lengths) {
-    for (int s = 0; s < a.S; ++s) d.total += visible_of(a, s).count();
-  } else {
-    d.total = a.S * visible_of(a, 0).count();
-  }
-  d.total *= a.Hkv;
+  d.total = blocks_before<kRagged>(a, a.S) * a.Hkv;
   d.W = min(W, d.total);  // every worker that counts owns a block
   d.q = d.W ? d.total / d.W : 0;
   d.r = d.total - d.q * d.W;
@@ -217,7 +243,11 @@ __device__ __forceinline__ void join_text(const WindowArgs& a, int L, int s, int
   }
 }
 
-template <typename T, int D, int NT, int NS, bool kAlone>
+// How a call is shared out: over the workers (one length, or lengths on the device),
+// or a thread block alone for each (stream, KV head).
+enum Share { kEven, kRagged, kOwn };
+
+template <typename T, int D, int NT, int NS, Share kShare>
 __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
   using B = Q4Block<D>;
   constexpr int kWarps = warps_of<NT, NS>();
@@ -226,6 +256,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
   constexpr int MT = D / 16;          // 16-channel tiles of O
   constexpr int kRows = 8 * NT;
   constexpr int kStride = D + 4;      // padded row of the partials in shared memory
+  constexpr bool kAlone = kShare == kOwn;
   constexpr bool kCentred = NS == 2;  // codes as c - 8, else as subnormals
   // S^T and O^T are in units of kUnit: with Q (P s) 16 times larger where the code is c 2^-22
   constexpr float kCodeNear = 0x1p-18f, kCodeFar = 0x1p-22f, kUnit = kCentred ? 1.f : kCodeNear;
@@ -255,10 +286,11 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
   pdl_trigger();
   int x = 0, x_end = 1, s = kAlone ? blockIdx.x / a.Hkv : 0, s_base = 0;
   if (!kAlone) {
-    const Deal deal = deal_of(a, p.W);
+    const Deal deal = deal_of<kShare == kRagged>(a, p.W);
     if ((int)blockIdx.x >= deal.W) return;
     x = deal.first(blockIdx.x);
     x_end = deal.first(blockIdx.x + 1);
+    s = stream_of<kShare == kRagged>(a, x, s_base);
   }
   Visible vis = visible_of(a, s);
   // text tokens of the tile's rows (rows behind R take the last one)
@@ -732,7 +764,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 // KV head and the visible text tokens, dealt to eight warps, each with its own
 // running maximum; then the eight are joined in order.
 constexpr int kMergeWarps = 8;
-template <typename T, int D>
+template <typename T, int D, bool kRaggedLengths>
 __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p) {
   constexpr int E = D / 32;  // channels per lane
   __shared__ float s_acc[kMergeWarps][D];
@@ -756,14 +788,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
     r = row % 128;
     w1 = p.W - 1;
   } else if (vis.count() > 0) {
-    const Deal deal = deal_of(a, p.W);
-    int base = 0;
-    if (a.lengths) {
-      for (int s2 = 0; s2 < s; ++s2) base += visible_of(a, s2).count();
-    } else {
-      base = s * vis.count();
-    }
-    base = base * a.Hkv + g * vis.count();
+    const Deal deal = deal_of<kRaggedLengths>(a, p.W);
+    const int base = blocks_before<kRaggedLengths>(a, s) * a.Hkv + g * vis.count();
     w0 = deal.owner(base);
     w1 = deal.owner(base + vis.count() - 1);
     part0 = (long long)(row / p.rows) * (p.W + a.S * a.Hkv) + sg;
@@ -818,24 +844,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
 template <typename T, int D>
 cudaError_t launch_merge(const Q4AttnArgs& p, cudaStream_t st) {
   const long long rows = (long long)p.w.S * p.w.Hq * p.w.n;
-  return launch_kernel(q4_merge_kernel<T, D>, dim3((unsigned)rows), dim3(kMergeWarps * 32), 0, st, true, p);
+  return launch_kernel(p.w.lengths ? q4_merge_kernel<T, D, true> : q4_merge_kernel<T, D, false>, dim3((unsigned)rows),
+                       dim3(kMergeWarps * 32), 0, st, true, p);
 }
 
-template <typename T, int D, int NT, int NS, bool kAlone>
+template <typename T, int D, int NT, int NS, Share kShare>
 cudaError_t launch_as(const Q4AttnArgs& p, unsigned workers, cudaStream_t st) {
   using B = Q4Block<D>;
   constexpr int kWarps = warps_of<NT, NS>();
   constexpr int ring = kWarps * kStages * B::kBytes;
   constexpr int merge = (kWarps * (D + 4 + 2) + 2) * 8 * NT * 4;
   constexpr int smem = ring > merge ? ring : merge;
-  const cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS, kAlone>, smem);
+  const cudaError_t e = ensure_dynamic_smem(q4_attn_kernel<T, D, NT, NS, kShare>, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(q4_attn_kernel<T, D, NT, NS, kAlone>, dim3(workers, p.n_rb), dim3(kWarps * 32), smem, st, false, p);
+  return launch_kernel(q4_attn_kernel<T, D, NT, NS, kShare>, dim3(workers, p.n_rb), dim3(kWarps * 32), smem, st, false, p);
 }
 template <typename T, int D, int NT, int NS>
 cudaError_t launch(const Q4AttnArgs& p, cudaStream_t st) {
-  if (p.W == 0) return launch_as<T, D, NT, NS, true>(p, p.w.S * p.w.Hkv, st);
-  const cudaError_t e = launch_as<T, D, NT, NS, false>(p, p.W, st);
+  if (p.W == 0) return launch_as<T, D, NT, NS, kOwn>(p, p.w.S * p.w.Hkv, st);
+  const cudaError_t e = p.w.lengths ? launch_as<T, D, NT, NS, kRagged>(p, p.W, st) : launch_as<T, D, NT, NS, kEven>(p, p.W, st);
   return e != cudaSuccess ? e : launch_merge<T, D>(p, st);
 }
 
@@ -872,8 +899,21 @@ Q4Plan q4_plan(int S, int Hq, int Hkv, int n, int dtype, int d, int n_sm) {
   return pl;
 }
 
+// One thread block per (stream, KV head, row tile) that takes all of its blocks,
+// joins the text tokens and writes the results (no partials, no second launch), or
+// the blocks dealt evenly to W workers and merged?  In units of what a block costs a
+// worker (some 0.11 us), with b blocks each for P pairs: ceil(P / W) rounds of 49 + b
+// against 68 once and 60 + b a pair, over W (lengths known to the device alone: P / W
+// + 1/4 rounds).  Measured (d = 128, G = 7, us, own
+// against dealt): 4 pairs of 1, 10, 32 blocks 5.7 : 6.8, 6.6 : 7.2, 8.8 : 7.9; 152
+// pairs of 64, 256 24 : 24, 69 : 52; 256 pairs 25 : 36, 72 : 78; 300 pairs 36 : 42,
+// 102 : 91; 400 pairs 43 : 57, 106 : 116; 1024 pairs of up to 32, ragged, 55 : 122.
 bool q4_alone(const WindowArgs& a, const Q4Plan& pl) {
-  return pl.rows != 128 && most_blocks(a) <= kAloneBlocks && a.n <= kAloneText && (long long)a.S * a.Hkv <= pl.W;
+  if (pl.rows == 128 || a.n > kOwnText) return false;
+  const long long b = most_blocks(a), pairs = (long long)a.S * a.Hkv, W = pl.W;
+  // rounds x 4 W; of different lengths they overlap
+  const long long rounds = a.lengths ? std::max(4 * W, 4 * pairs + W) : (pairs + W - 1) / W * 4 * W;
+  return rounds * (49 + b) <= 4 * (68 * W + (60 + b) * pairs);
 }
 
 cudaError_t launch_q4_attn(const WindowArgs& a, const Q4Plan& pl, void* workspace, int dtype, int d, cudaStream_t st) {

@@ -757,8 +757,8 @@ def test_sink_window_prefill_f32_of_the_largest_values(d):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,window,n_sink", [(1, 0, 0), (3, 0, 0), (3, 90, 5)])
 def test_decode_is_the_same_on_either_side_of_a_kernel_border(n, window, n_sink, dtype):
-    """768 cached tokens (one block per KV head), 769 (shared out and merged) and, in
-    a cache whose lengths only the device knows, both."""
+    """300 cached tokens (one block per KV head), 799 (shared out and merged) and, in
+    a cache whose lengths only the device knows, different ones."""
     S, Hq, Hkv, d = 2, 8, 2, 64
     pk, pv = tokens(1, S, 800, Hkv, d, dtype)
     k, v = tokens(2, S, n, Hkv, d, dtype)
@@ -768,7 +768,7 @@ def test_decode_is_the_same_on_either_side_of_a_kernel_border(n, window, n_sink,
     c.append(pk.cuda(), pv.cuda(), 0)
     hk, hv = O.q4_held(pk), O.q4_held(pv)
     lens = torch.tensor([768, 0], dtype=torch.int32, device="cuda")
-    for at, of in ((768, [768] * 2), (769, [769] * 2), (lens, [768, 0])):
+    for at, of in ((300, [300] * 2), (799, [799] * 2), (lens, [768, 0])):
         out, lse = c.decode(*ins, at, window=window, n_sink=n_sink)
         for s in range(S):
             want = reference(q[s], k[s], v[s], hk[s, :of[s]], hv[s, :of[s]], window, n_sink)
@@ -797,3 +797,27 @@ def test_decode_f32_of_a_long_cache_keeps_its_precision(d):
     want = torch.einsum("shij,sjhd->sihd", w, V)
     rel = ((out.double() - want).norm() / want.norm()).item()
     assert rel <= 2.0 ** -19, f"{rel:.3g}"
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (200, 40)])
+def test_decode_of_many_streams_of_different_lengths(window, n_sink, dtype):
+    """75 streams, a third of them empty, the last ones too, shared out over the
+    workers: every stream meets its own tokens."""
+    S, Hq, Hkv, d, cap, n = 75, 4, 2, 64, 900, 1
+    g = torch.Generator().manual_seed(7)
+    lens = torch.randint(0, cap + 1, (S,), generator=g, dtype=torch.int32)
+    lens[::3] = 0
+    lens[-2:] = 0
+    pk, pv = tokens(1, S, cap, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    c = _skv().Q4Cache(Hkv, d, cap, n_streams=S)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), lens.cuda(), window=window, n_sink=n_sink)
+    hk, hv = O.q4_held(pk), O.q4_held(pv)
+    for s in range(S):
+        L = int(lens[s])
+        want = reference(q[s], k[s], v[s], hk[s, :L], hv[s, :L], window, n_sink)
+        check_attention(out[s], lse[s], want, dtype, 2.0 ** -11 if dtype == "bf16" else 0.0)
