@@ -37,10 +37,12 @@
 // The visible 32-token blocks of all (stream, KV head) are numbered in order
 // and dealt evenly to the W workers (thread blocks), so ragged streams balance;
 // a worker writes one partial (max, sum, O) per (stream, KV head) it meets, and
-// q4_merge_kernel joins them in worker order with the text tokens' own part.
+// q4_merge_kernel joins them in worker order with the text tokens' own part.  Where
+// it is cheaper (q4_alone) each (stream, KV head) has a thread block of its own, which
+// writes the results itself.
 //
 // Measured (B200, graph replays, bf16, d = 128, G = 7, one text token, caches beyond
-// L2): 4 ragged streams of up to 131072 tokens, 4 KV heads, 56.5 us (4.3 TB/s of
+// L2): 4 ragged streams of up to 131072 tokens, 4 KV heads, 55.5 us (4.4 TB/s of
 // the cache; 245 MB would take 37.4 at the copy rate), 131072 tokens of one stream
 // 26.7 us (75 MB: 11.5).  About 8 us of each are the first copies' latency and the
 // merge; the loop streams at some 5 TB/s, the tensor-core and integer pipes each
