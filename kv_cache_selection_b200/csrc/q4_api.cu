@@ -2,6 +2,7 @@
 // sink_window_prefill: argument checks and launches (include/statekv.h).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -258,8 +259,9 @@ int sink_window_prefill_batched(const void* q, const void* k, const void* v, int
   a.S = n_seq;
   a.Hq = Hq;
   a.Hkv = Hkv;
-  a.window = window;
-  a.n_sink = n_sink;
+  // more than all tokens is all tokens (the kernels round both up to tiles)
+  a.window = std::min(window, n_tokens);
+  a.n_sink = std::min(n_sink, n_tokens);
   a.scale_log2 = skv::kLog2e / sqrtf((float)d);
   const cudaError_t e = dtype == STATEKV_BF16 ? skv::launch_window_tc(a, d, static_cast<cudaStream_t>(stream))
                                               : skv::launch_window_f32(a, d, static_cast<cudaStream_t>(stream));

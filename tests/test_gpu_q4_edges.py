@@ -1,0 +1,75 @@
+"""The 4-bit cache's decode and sink_window_prefill at the edges of what a call
+may hold: the largest windows and sink counts, infinite keys, values that only
+some rows see, values and keys next to the largest float, NaN inputs, many
+streams.  Inputs, limits and the oracle are those of test_gpu_q4.py; for decodes
+`mass` is taken of what the kernels round, the parts of a held value
+v = (c - 8) s + mid, mid = m + 8 s:
+  * up to 32 rows: P s is rounded, 2^-11 (or 2^-22) of P |(c - 8) s|, which is
+    at most P (|v| + |mid|);
+  * more rows in bf16: P, the value and mid are rounded, 2^-11 of P |v|, P |v| and
+    P |mid|;
+so mass = sum_j p_j (2 |v_j| + |mid_j|) bounds both."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import statekv_oracle as O
+from tests.test_gpu_q4 import DT, Want, _skv, check_attention, cuda, reference, same, tokens
+
+pytestmark = pytest.mark.gpu
+
+P_DECODE = {"bf16": 2.0 ** -11, "f32": 0.0}
+P_PREFILL = {"bf16": 2.0 ** -8, "f32": 0.0}
+INT_MAX = 2 ** 31 - 1
+
+
+def part_of(want, rows):
+    w = Want((want[0][rows], want[1][:, rows], want[2][rows], want[3][:, rows]))
+    w.keys = want.keys
+    return w
+
+
+def decode_reference(q, k, v, pk, pv, window, n_sink):
+    """reference() over the tokens that a cache holds for pk, pv [L][Hkv][d]."""
+    if pk.shape[0] == 0:
+        return reference(q, k, v, None, None, window, n_sink)
+    w = reference(q, k, v, O.q4_held(pk), O.q4_held(pv), window, n_sink)
+    _, s, m = O.q4_codes(pv)
+    mid = np.repeat(np.abs(m + 8 * s), 64, -1).reshape(pv.shape)
+    mid_mass = O.window_attention(q, k, torch.zeros(v.shape), O.q4_held(pk), mid, window, n_sink)[2]
+    full = Want((w[0], w[1], 2 * w[2] + mid_mass, w[3]))
+    full.keys = w.keys
+    return full
+
+
+# ------------------------------------------------------- the largest arguments
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,n_sink", [(INT_MAX, 0), (1, INT_MAX), (50, INT_MAX - 126), (INT_MAX, INT_MAX)])
+def test_sink_window_prefill_of_the_largest_windows(window, n_sink, d, dtype):
+    """2^31 - 1 as "all tokens", in the window and in the first tokens."""
+    n, Hq, Hkv = 391, 2, 1
+    k, v = tokens(1, 1, n, Hkv, d, dtype)
+    q, _ = tokens(2, 1, n, Hq, d, dtype, loud=False)
+    out = torch.full((1, n, Hq, d), float("nan"), dtype=DT[dtype], device="cuda")
+    lse = torch.full((1, Hq, n), float("nan"), device="cuda")
+    _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=n_sink, out=out, lse=lse)
+    check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, 0, 0), dtype, P_PREFILL[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("window,n_sink", [(INT_MAX, 0), (1, INT_MAX), (50, INT_MAX - 30), (INT_MAX, INT_MAX)])
+def test_decode_of_the_largest_windows(window, n_sink, n, dtype):
+    S, Hq, Hkv, d, L = 1, 8, 2, 64, 333
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    c = _skv().Q4Cache(Hkv, d, L + 5)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L, window=window, n_sink=n_sink)
+    check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0], pv[0], 0, 0), dtype,
+                    P_DECODE[dtype])
