@@ -22,10 +22,10 @@
 // S was left in, with its keys as the depth.
 //
 // The running maximum starts at -inf; a weight whose key is hidden is -0, which
-// adds nothing to a sum.  Where a tile holds a value that is not finite (or too
-// close to the largest float32 to be rounded) that value is 0 in the product, and
-// the rows that see it add it afterwards: hidden values never take part, and the
-// other sums keep their bits.
+// adds nothing to a sum.  Where a tile holds a key or value that is not finite (or
+// too close to the largest float32 to be rounded) that number is 0 in the product,
+// and the rows that see it add it afterwards: hidden values never take part, and
+// the other sums keep their bits.
 #include <type_traits>
 
 #include "common.cuh"
@@ -65,8 +65,9 @@ __device__ __forceinline__ void mma_parts(float (&c)[4], const uint32_t (&a)[2][
   mma_tf32(c, a[0], b[0]);
 }
 
-// x as hi + lo (the tensor cores read the upper 19 bits of lo).  kAny: x may be a
-// NaN, an infinity (hi is, lo is 0) or above kBig (hi is cut, not rounded).
+// x as hi + lo (the tensor cores read the upper 19 bits of lo).  kAny: x (of a query)
+// may be a NaN, an infinity (hi is, lo is 0; every logit of the row is one of the two
+// then) or above kBig (hi is cut, not rounded).
 template <bool kAny>
 __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
   const uint32_t b = __float_as_uint(x);
@@ -178,12 +179,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
         split<true>(x1.w, qb[0][3], qb[1][3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float4 y = *reinterpret_cast<const float4*>(kt + (t * 8 + gid) * L::kKStride + p * 16 + tig * 4);
+          const float4 y4 = *reinterpret_cast<const float4*>(kt + (t * 8 + gid) * L::kKStride + p * 16 + tig * 4);
+          float y[4] = {y4.x, y4.y, y4.z, y4.w};
+          if (kAny) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(fabsf(y[i]) < kBig)) y[i] = 0.f;
+          }
           uint32_t ya[2][2], yb[2][2];
-          split<kAny>(y.x, ya[0][0], ya[1][0]);
-          split<kAny>(y.y, ya[0][1], ya[1][1]);
-          split<kAny>(y.z, yb[0][0], yb[1][0]);
-          split<kAny>(y.w, yb[0][1], yb[1][1]);
+          split<false>(y[0], ya[0][0], ya[1][0]);
+          split<false>(y[1], ya[0][1], ya[1][1]);
+          split<false>(y[2], yb[0][0], yb[1][0]);
+          split<false>(y[3], yb[0][1], yb[1][1]);
           float acc[4] = {0.f, 0.f, 0.f, 0.f};
           mma_parts(acc, qa, ya);
           mma_parts(acc, qb, yb);
@@ -192,8 +199,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
         }
       }
     };
-    if (careful) scores(std::true_type());
-    else scores(std::false_type());
+    if (!careful) {
+      scores(std::false_type());
+    } else {
+      scores(std::true_type());
+      // what was 0 in the products, times q as it is: in parts an infinite key would
+      // meet q's low part, which is 0 or of the other sign as often as not
+#pragma unroll 1
+      for (int x = 0; x < 2 * NT; ++x) {  // this lane's keys
+        const float* row = kt + ((x >> 1) * 8 + tig * 2 + (x & 1)) * L::kKStride;
+        const float* q0 = smem + L::kQ + (warp * 16 + gid) * L::kKStride;
+        float add[2] = {0.f, 0.f};
+#pragma unroll 1
+        for (int c = 0; c < D; ++c) {
+          const float y = row[c];
+          if (fabsf(y) < kBig) continue;
+          add[0] = fmaf(q0[c], y, add[0]);
+          add[1] = fmaf(q0[8 * L::kKStride + c], y, add[1]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (x == 2 * t + b) {
+              sc[t][b] += add[0];
+              sc[t][2 + b] += add[1];
+            }
+      }
+    }
 
     // ---- softmax: element e of tile t is row r0 + 8 (e/2), key 8 t + 2 tig + e%2
     const bool masked = base + KT > w0 + 1 || (base <= w0 + 15 - a.window && base + KT > a.n_sink);

@@ -73,3 +73,33 @@ def test_decode_of_the_largest_windows(window, n_sink, n, dtype):
     out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L, window=window, n_sink=n_sink)
     check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0], pv[0], 0, 0), dtype,
                     P_DECODE[dtype])
+
+
+# --------------------------------------------------------------- infinite keys
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_sink_window_prefill_of_infinite_keys(sign, d, dtype):
+    """An infinite channel of a key that rows see.  Head 0's queries give it a
+    logit of -inf: it weighs nothing, the row is what the other keys make it.
+    Head 1's give +inf, head 2's 0 x inf: NaN by definition."""
+    n, Hq, Hkv, window, at = 260, 3, 1, 70, 100
+    k, v = tokens(1, 1, n, Hkv, d, dtype)
+    q, _ = tokens(2, 1, n, Hq, d, dtype, loud=False)
+    q[..., 0, 7] = -sign * (q[..., 0, 7].abs() + 0.1)
+    q[..., 1, 7] = sign * (q[..., 1, 7].abs() + 0.1)
+    q[..., 2, 7] = 0.0
+    clean = reference(q[0], k[0], v[0], None, None, window, 2)
+    k[0, at, 0, 7] = sign * float("inf")
+    out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)
+    far = k.clone()
+    far[0, at, 0, 7] = sign * 1e30           # head 0: a logit below -1e28, a weight of 0 as well
+    w = reference(q[0], far[0], v[0], None, None, window, 2)
+    sees = slice(at, at + window)
+    want = Want((w[0][:, :1], w[1][:1], w[2][:, :1], clean[3][:1]))   # (limits of the finite logits)
+    want.keys = n
+    check_attention(out[0, :, :1], lse[0, :1], want, dtype, P_PREFILL[dtype])
+    assert torch.isnan(out[0, sees, 1:]).all() and torch.isnan(lse[0, 1:, sees]).all()
+    for rows in (slice(0, at), slice(at + window, n)):
+        check_attention(out[0, rows], lse[0][:, rows], part_of(clean, rows), dtype, P_PREFILL[dtype])
