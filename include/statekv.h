@@ -385,7 +385,9 @@ int statekv_q4_read(const void* cache, int n_streams, int Hkv, int d, int capaci
  * above L + i - window and those below n_sink (window = 0: no window, n_sink
  * unused).  Scale 1/sqrt(d).  A key or value the mask hides has no influence,
  * whatever it holds.  The text tokens are not written to the cache; their own
- * part is computed row by row, so its work grows with n_text squared.
+ * part, and that of the n_text - 1 cache tokens at most that the window hides
+ * from some of them, is computed row by row, so its work grows with n_text
+ * squared.
  * bf16 calls hold a weight times its value's scale in fp16, relative to the
  * largest so far of a row's weights and of the visible scales: 2^-11 of it, and
  * what is below 2^-29 of the largest counts as 0.  float32 calls hold it in two

@@ -37,9 +37,10 @@
 // The visible 32-token blocks of all (stream, KV head) are numbered in order
 // and dealt evenly to the W workers (thread blocks), so ragged streams balance;
 // a worker writes one partial (max, sum, O) per (stream, KV head) it meets, and
-// q4_merge_kernel joins them in worker order with the text tokens' own part.  Where
-// it is cheaper (q4_alone) each (stream, KV head) has a thread block of its own, which
-// writes the results itself.
+// q4_merge_kernel joins them in worker order with what a row sees on its own: the
+// text tokens and, with a window, the cache tokens that later rows of its tile do not
+// see (q4_visible.cuh).  Where it is cheaper (q4_alone) each (stream, KV head) has a
+// thread block of its own, which writes the results itself.
 //
 // Measured (B200, graph replays, bf16, d = 128, G = 7, one text token, caches beyond
 // L2): 4 ragged streams of up to 131072 tokens, 4 KV heads, 55.5 us (4.4 TB/s of
@@ -219,30 +220,64 @@ struct RowSum {
     m = nm;
   }
 };
-// The text tokens first, first + step, ... that the row (text token i, head h) sees.
+// What the row (text token i, head h) sees beside the cache tokens of its whole tile:
+// cache tokens behind its own window's edge and before that of the tile's last
+// text token, and the text tokens; of both the ones first, first + step, ...
 template <typename T, int D>
-__device__ __forceinline__ void join_text(const WindowArgs& a, int L, int s, int h, int g, int i, int first, int step,
-                                          RowSum<D / 32>& sum) {
+__device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int h, int g, int i, int i_last, int first,
+                                         int step, RowSum<D / 32>& sum) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const T* q = static_cast<const T*>(a.q) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
   float qv[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) qv[e] = to_f(q[e]) * a.scale_log2;
-  for (int j = first; j <= i; j += step) {
-    if (a.window && j <= i - a.window && (long long)L + j >= a.n_sink) continue;
+  // four tokens' loads and sums over the lanes at once, then one by one
+  auto run = [&](int j, int end, auto load) {
+    auto some = [&](auto count) {
+      constexpr int N = decltype(count)::value;
+      float t[N], k[N][E], v[N][E];
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        load(j + b * step, k[b], v[b]);
+        t[b] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[b] = fmaf(qv[e], k[b][e], t[b]);
+      }
+#pragma unroll
+      for (int off = 16; off; off >>= 1)
+#pragma unroll
+        for (int b = 0; b < N; ++b) t[b] += __shfl_xor_sync(0xffffffffu, t[b], off);
+#pragma unroll
+      for (int b = 0; b < N; ++b) {
+        if (t[b] != t[b]) sum.l = t[b];  // a NaN logit makes the row NaN
+        sum.join(t[b], 1.f, v[b]);
+      }
+      j += N * step;
+    };
+    while (j < end - 3 * step) some(std::integral_constant<int, 4>());
+    while (j < end) some(std::integral_constant<int, 1>());
+  };
+  if (a.window) {
+    const int end = tile_from(a, L, i_last);
+    const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * Q4Block<D>::kBytes;
+    run(max(row_from(a, L, i), min(a.n_sink, end)) + first, end, [&](int j, float (&k)[E], float (&v)[E]) {
+      q4_token<D, E>(cache + (long long)(j / kQ4Tokens) * Q4Block<D>::kBytes, j % kQ4Tokens, lane * E, k, v);
+    });
+  }
+  auto text = [&](int j, float (&k)[E], float (&v)[E]) {
     const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
-    float t = 0.f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      t = fmaf(qv[e], to_f(static_cast<const T*>(a.k)[at + e]), t);
+      k[e] = to_f(static_cast<const T*>(a.k)[at + e]);
       v[e] = to_f(static_cast<const T*>(a.v)[at + e]);
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    if (t != t) sum.l = t;  // a NaN logit makes the row NaN
-    sum.join(t, 1.f, v);
-  }
+  };
+  // text tokens: the first ones below n_sink, and those of the window
+  const int sinks = a.window ? (int)min(max((long long)a.n_sink - L, 0ll), i + 1ll) : 0;
+  const int from = a.window ? max(sinks, i - a.window + 1) : 0;
+  run(first, sinks, text);
+  run(from + first, i + 1, text);
 }
 
 // How a call is shared out: over the workers (one length, or lengths on the device),
@@ -295,8 +330,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     s = stream_of<kShare == kRagged>(a, x, s_base);
   }
   Visible vis = visible_of(a, s);
-  // text tokens of the tile's rows (rows behind R take the last one)
-  const int i_first = row0 / G, i_last = (min(row0 + kRows, R) - 1) / G;
+  const int i_last = tile_last(blockIdx.y, kRows, R, G);
 
   while (x < x_end) {
     int g = blockIdx.x % a.Hkv, v0 = 0, v1 = vis.count();
@@ -343,7 +377,6 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     // ---- Q fragments, per-row scale and group sums
     uint32_t qf[NT][NS][MT][2];
     float qsum[NT][NG][2], rs[NT][2];
-    int irow[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = 0.f;
@@ -389,7 +422,6 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) qsum[nt][gg][e] = __shfl_sync(0xffffffffu, sum[gg], from);
         rs[nt][e] = __shfl_sync(0xffffffffu, down, from) * a.scale_log2;
-        irow[nt][e] = min(row0 + nt * 8 + 2 * tig + e, R - 1) / G;
       }
     }
 
@@ -423,15 +455,14 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
       vs[gg] = kPScale / kMinR;
     }
 
+    const int from = tile_from(a, vis.L, i_last);
     for (int v = v0 + warp; ok && v < v1; v += kWarps, ++done) {
       const int stage = done % kStages;
       const uint32_t bar = bars + 8u * stage, parity = (done / kStages) & 1;
       if (!(ok = tc::warp_wait_all(bar, parity, &g_err, tc::kErrWaitLoad, abort_flag))) break;
       const uint8_t* blk = ring + stage * B::kBytes;
       const int t0 = vis.block(v) * kQ4Tokens;
-      bool full = t0 + kQ4Tokens <= vis.L;
-      if (a.window)
-        full = full && (t0 > vis.L + i_last - a.window || t0 + kQ4Tokens <= a.n_sink);
+      const bool full = t0 + kQ4Tokens <= vis.L && (t0 >= from || t0 + kQ4Tokens <= a.n_sink);
       // ---- S^T = K Q^T, 16 tokens at a time; t rs = logits in log2 units
       float t[NT][2][4];
 #pragma unroll
@@ -510,26 +541,18 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
             mv[kt][hh][gg] = fmaf(sv[kt][hh][gg], 8.f, q4_min(sm));
           }
         }
-      // ---- masks: hidden tokens get a logit of -inf; a V scale no row uses gets 0
+      // ---- masks: hidden tokens get a logit of -inf and a V scale of 0
       if (!full) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const int tok = t0 + kt * 16 + hh * 8 + gid;
-            const bool in = tok < vis.L;
-            const bool keep = !a.window || tok < a.n_sink;
-            if (!(in && (keep || tok > vis.L + i_first - a.window))) {
+            if (tok < vis.L && (tok >= from || tok < a.n_sink)) continue;
 #pragma unroll
-              for (int gg = 0; gg < NG; ++gg) sv[kt][hh][gg] = mv[kt][hh][gg] = 0.f;
-            }
+            for (int gg = 0; gg < NG; ++gg) sv[kt][hh][gg] = mv[kt][hh][gg] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const bool ok = in && (keep || tok > vis.L + irow[nt][e] - a.window);
-                if (!ok) t[nt][kt][hh * 2 + e] = -INFINITY;
-              }
+            for (int nt = 0; nt < NT; ++nt) t[nt][kt][hh * 2] = t[nt][kt][hh * 2 + 1] = -INFINITY;
           }
       }
       // ---- lazy row maximum and V reference
@@ -590,51 +613,32 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
       }
       // ---- P, its sums, and P s as fp16 fragments
       uint32_t pf[NT][NS][NG][2][2];
-      auto weights = [&](auto careful) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const float p0 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2], rs[nt][0], -mr[nt][0]));
-              const float p1 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2 + 1], rs[nt][1], -mr[nt][1]));
-              l[nt][0] += p0;
-              l[nt][1] += p1;
-#pragma unroll
-              for (int gg = 0; gg < NG; ++gg) {
-                // tokens of fields 0 and 3 (kt == hh): 16 times less
-                float s0 = sv[kt][hh][gg] * (!kCentred && kt == hh ? vs[gg] * (kCodeFar / kCodeNear) : vs[gg]), s1 = s0, m0v = mv[kt][hh][gg], m1v = m0v;
-                if (careful) {  // (the same roundings with and without)
-                  if (t[nt][kt][hh * 2] == -INFINITY) s0 = m0v = 0.f;
-                  if (t[nt][kt][hh * 2 + 1] == -INFINITY) s1 = m1v = 0.f;
-                }
-                const float x0 = p0 * s0, x1 = p1 * s1;
-                corr[nt][gg][0] = fmaf(p0, m0v, corr[nt][gg][0]);
-                corr[nt][gg][1] = fmaf(p1, m1v, corr[nt][gg][1]);
-                const __half2 hi = __floats2half2_rn(x0, x1);
-                pf[nt][0][gg][kt][hh] = transpose8x8(half2_bits(hi));
-                if (NS == 2) {
-                  const float2 h = __half22float2(hi);
-                  pf[nt][NS - 1][gg][kt][hh] = transpose8x8(half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y)));
-                }
-              }
-            }
-        }
-      };
-      // a NaN scale of a token that only some rows see stays out of the others
-      bool odd = false;
-      if (!full) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
+          for (int hh = 0; hh < 2; ++hh) {
+            const float p0 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2], rs[nt][0], -mr[nt][0]));
+            const float p1 = tc::ex2_approx(fmaf(t[nt][kt][hh * 2 + 1], rs[nt][1], -mr[nt][1]));
+            l[nt][0] += p0;
+            l[nt][1] += p1;
 #pragma unroll
-            for (int gg = 0; gg < NG; ++gg) odd |= mv[kt][hh][gg] != mv[kt][hh][gg];
-        odd = __any_sync(0xffffffffu, odd);
+            for (int gg = 0; gg < NG; ++gg) {
+              // tokens of fields 0 and 3 (kt == hh): 16 times less
+              const float s0 = sv[kt][hh][gg] * (!kCentred && kt == hh ? vs[gg] * (kCodeFar / kCodeNear) : vs[gg]);
+              const float x0 = p0 * s0, x1 = p1 * s0;
+              corr[nt][gg][0] = fmaf(p0, mv[kt][hh][gg], corr[nt][gg][0]);
+              corr[nt][gg][1] = fmaf(p1, mv[kt][hh][gg], corr[nt][gg][1]);
+              const __half2 hi = __floats2half2_rn(x0, x1);
+              pf[nt][0][gg][kt][hh] = transpose8x8(half2_bits(hi));
+              if (NS == 2) {
+                const float2 h = __half22float2(hi);
+                pf[nt][NS - 1][gg][kt][hh] = transpose8x8(half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y)));
+              }
+            }
+          }
       }
-      if (odd) weights(std::true_type());
-      else weights(std::false_type());
       // ---- the weights' own sums, then O^T += V^T P^T, 32 channels at a time
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -737,7 +741,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
       *reinterpret_cast<float4*>(kAlone ? wo + r * kStride + c * 4 : p.part_o + (part * kRows + r) * D + c * 4) = acc;
       if (c == 0) *reinterpret_cast<float2*>(kAlone ? row_ml + r * 2 : p.part_ml + (part * kRows + r) * 2) = make_float2(mx, ls);
     }
-    if (kAlone) {  // a warp per row: its sum, then the text tokens
+    if (kAlone) {  // a warp per row: its sum, then its own tokens
       __syncthreads();
       constexpr int E = D / 32;
       for (int r = warp; r < min(kRows, R - row0); r += kWarps) {
@@ -747,7 +751,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
         sum.l = row_ml[r * 2 + 1];
 #pragma unroll
         for (int e = 0; e < E; ++e) sum.acc[e] = wo[r * kStride + lane * E + e];
-        join_text<T, D>(a, vis.L, s, h, g, i, 0, 1, sum);
+        join_own<T, D>(a, vis.L, s, h, g, i, i_last, 0, 1, sum);
         T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) out[e] = from_f<T>(sum.acc[e] / sum.l);
@@ -763,8 +767,8 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 }
 
 // One block per (stream, query head, text token): the workers' partials of its
-// KV head and the visible text tokens, dealt to eight warps, each with its own
-// running maximum; then the eight are joined in order.
+// KV head and the row's own tokens (join_own), dealt to eight warps, each with its
+// own running maximum; then the eight are joined in order.
 constexpr int kMergeWarps = 8;
 template <typename T, int D, bool kRaggedLengths>
 __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p) {
@@ -778,9 +782,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
   const int i = (int)(rw % a.n), h = (int)(rw / a.n % a.Hq), s = (int)(rw / a.n / a.Hq);
   const int g = h / G, row = i * G + h % G;
   RowSum<E> sum;
-  // the call's own tokens (inputs of the call: read before the wait)
+  // the row's own tokens (inputs of the call: read before the wait)
   const Visible vis = visible_of(a, s);
-  join_text<T, D>(a, vis.L, s, h, g, i, warp, kMergeWarps, sum);
+  join_own<T, D>(a, vis.L, s, h, g, i, tile_last(row / p.rows, p.rows, G * a.n, G), warp, kMergeWarps, sum);
   // where the partials are
   int w0 = 0, w1 = -1, r = 0;
   long long part0 = 0;

@@ -68,8 +68,7 @@ struct Smem {
   static constexpr int kTab = kRawAt + kRaw * kRawTile;
   static constexpr int kHalfMax = kTab + kTabBytes;  // [2][128] float32
   static constexpr int kTop = kHalfMax + 1024;           // largest magnitudes of K, V (float32 bits)
-  static constexpr int kPoison = kTop + 16;              // [4 tiles][groups][4 words]
-  static constexpr int kBar = kPoison + 4 * B::kGroups * 16;
+  static constexpr int kBar = kTop + 16;
   // read before the second K tile is written: row scales [128], group sums of q [128][groups]
   static constexpr int kRow = kK + kTile;
   static constexpr int kQs = kRow + 512;
@@ -125,18 +124,10 @@ __device__ __forceinline__ uint32_t dequant(uint32_t x, uint32_t s, uint32_t mid
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
 
-// Token `at` of the visible block number v: seen by some row of the tile, by
-// every row of the tile.
-struct Token {
-  bool some, every;
-};
-__device__ __forceinline__ Token token_of(const WindowArgs& a, const Visible& vis, int v, int at, int i_first, int i_last) {
+// Do the rows of the tile see token `at` of the visible block number v?
+__device__ __forceinline__ bool seen_token(const WindowArgs& a, const Visible& vis, int from, int v, int at) {
   const int tok = v < vis.count() ? vis.block(v) * kQ4Tokens + at : 0x7fffffff;
-  const bool keep = !a.window || tok < a.n_sink;
-  Token t;
-  t.some = tok < vis.L && (keep || (long long)tok > (long long)vis.L + i_first - a.window);
-  t.every = keep || (long long)tok > (long long)vis.L + i_last - a.window;
-  return t;
+  return tok < vis.L && (tok >= from || tok < a.n_sink);
 }
 
 template <int D>
@@ -159,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   const int sg = u / p.n_rb;
   const int g = sg % a.Hkv, s = sg / a.Hkv;
   const int G = a.Hq / a.Hkv, R = G * a.n, row0 = rb * 128;
-  const int i_first = row0 / G, i_last = (min(row0 + 128, R) - 1) / G;
   const Visible vis = visible_of(a, s);
+  const int from = tile_from(a, vis.L, tile_last(rb, 128, R, G));
   const int tiles = (vis.count() + 3) / 4;
   const int t_begin = (int)((long long)tiles * sp / p.W), n = (int)((long long)tiles * (sp + 1) / p.W) - t_begin;
 
@@ -179,7 +170,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kTmem);
   uint32_t* tops = reinterpret_cast<uint32_t*>(smem + L::kTop);
   float* half_max = reinterpret_cast<float*>(smem + L::kHalfMax);
-  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPoison);
   int* err = &g_err;
 
   if (threadIdx.x == 0) {
@@ -231,14 +221,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     using Words = typename std::conditional<NG == 2, uint2, uint32_t>::type;
 #pragma unroll 8
     for (int x = t_begin * 4 * kQ4Tokens + mine; x < end; x += 480) {
-      const Token t = token_of(a, vis, x / kQ4Tokens, x % kQ4Tokens, i_first, i_last);
+      const bool seen = seen_token(a, vis, from, x / kQ4Tokens, x % kQ4Tokens);
       const uint8_t* blk = base + (long long)vis.block(x / kQ4Tokens) * B::kBytes + (x % kQ4Tokens) * (NG * 4);
       const Words kw = __ldg(reinterpret_cast<const Words*>(blk + B::kKs)), vw = __ldg(reinterpret_cast<const Words*>(blk + B::kVs));
 #pragma unroll
       for (int w = 0; w < 2 * NG; ++w) {
         const uint32_t sm = reinterpret_cast<const uint32_t*>(w < NG ? &kw : &vw)[w % NG];
         const float sc = q4_scale(sm), y = fmaf(sc, 8.f, fabsf(fmaf(sc, 8.f, q4_min(sm))));
-        if (t.some) top[w / NG] = fmaxf(top[w / NG], y);
+        if (seen) top[w / NG] = fmaxf(top[w / NG], y);
       }
     }
 #pragma unroll
@@ -365,9 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     const int half = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, row = row0 + r;
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16), t_o = t_lane + kColO + half * (D / 2);
     const bool real = row < R;
-    const int i = min(row, R - 1) / G;
     float m_used = -INFINITY, l = 0.f, c = 0.f;
-    uint32_t nan_groups = 0;
     bool ok = n > 0;
     if (ok) {
       c = reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK);
@@ -394,27 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       fence_after_sync();
       const uint32_t t_s = t_lane + col_s(j & 1) + half * 64;
       const int v0 = (t_begin + j) * 4;
-      bool full = v0 + 4 <= vis.count() && vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= vis.L;
-      if (a.window)
-        full = full && ((long long)vis.block(v0) * kQ4Tokens > (long long)vis.L + i_last - a.window ||
-                        vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= a.n_sink);
-      // V's poison words come with its tile
-      if (ok && !full) ok = warp_wait_all(v_full(j & 1), (j >> 1) & 1, err, kErrWaitLoad, abort_flag);
+      const bool full = v0 + 4 <= vis.count() && vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= vis.L &&
+                        (vis.block(v0) * kQ4Tokens >= from || vis.block(v0 + 3) * kQ4Tokens + kQ4Tokens <= a.n_sink);
       if (!full) {  // hidden columns of S become -inf in tensor memory
-        const long long from = a.window ? (long long)vis.L + i - a.window + 1 : 0;
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
-          const int vb = v0 + half * 2 + b;
-          const int t0 = vb < vis.count() ? vis.block(vb) * kQ4Tokens : 0x40000000;
-          uint32_t seen = 0;  // slots of the block that the row sees
+          uint32_t seen = 0;  // slots of the block that the rows see
 #pragma unroll 1
-          for (int q = 0; q < 32; ++q) {
-            const int tok = t0 + ((q & 7) >> 2) * 16 + ((q >> 1) & 1) * 8 + (q >> 3) * 2 + (q & 1);
-            if (tok < vis.L && (tok >= from || tok < a.n_sink)) seen |= 1u << q;
-          }
-#pragma unroll
-          for (int gg = 0; gg < NG; ++gg)
-            if (seen & poison[((j & 3) * NG + gg) * 4 + half * 2 + b]) nan_groups |= 1u << gg;
+          for (int q = 0; q < 32; ++q)
+            if (seen_token(a, vis, from, v0 + half * 2 + b, ((q & 7) >> 2) * 16 + ((q >> 1) & 1) * 8 + (q >> 3) * 2 + (q & 1)))
+              seen |= 1u << q;
           uint32_t sv[32];
           tmem_ld32(t_s + b * 32, sv);
           tmem_ld_wait_dep(sv);
@@ -504,13 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
         uint32_t v[32];
         tmem_ld32(t_o + c0 * 32, v);
         tmem_ld_wait_dep(v);
-        const float add = (nan_groups >> ((half * (D / 2) + c0 * 32) / kQ4Group) & 1) ? NAN : 0.f;
         if (real) {
           float4* dst = reinterpret_cast<float4*>(po + c0 * 32);
 #pragma unroll
           for (int q4 = 0; q4 < 8; ++q4)
-            dst[q4] = make_float4(fmaf(__uint_as_float(v[4 * q4]), back, add), fmaf(__uint_as_float(v[4 * q4 + 1]), back, add),
-                                  fmaf(__uint_as_float(v[4 * q4 + 2]), back, add), fmaf(__uint_as_float(v[4 * q4 + 3]), back, add));
+            dst[q4] = make_float4(__uint_as_float(v[4 * q4]) * back, __uint_as_float(v[4 * q4 + 1]) * back,
+                                  __uint_as_float(v[4 * q4 + 2]) * back, __uint_as_float(v[4 * q4 + 3]) * back);
         }
       }
     } else if (real) {  // no tiles (or an abandoned call): nothing to add
@@ -535,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       if (!warp_wait_all(raw_full(sl), (j / kRaw) & 1, err, kErrWaitLoad, abort_flag)) break;
       if (!warp_wait_all(k_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
       const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
-      const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);
+      const bool seen = seen_token(a, vis, from, (t_begin + j) * 4 + w4, tok_of);
       uint32_t s2[NG], x[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int gg = 0; gg < NG; ++gg) {
         const uint32_t sm = reinterpret_cast<const uint32_t*>(raw + B::kKs)[tok_of * NG + gg];
-        const float sc = t.some ? q4_scale(sm) * norm : 0.f;
-        const float y = t.some ? fmaf(q4_scale(sm), 8.f, q4_min(sm)) * norm * 4.f : 0.f;
+        const float sc = seen ? q4_scale(sm) * norm : 0.f;
+        const float y = seen ? fmaf(q4_scale(sm), 8.f, q4_min(sm)) * norm * 4.f : 0.f;
         const float hi = __half2float(__float2half_rn(y));
         s2[gg] = pack_half2(sc, sc);
         x[2 * gg] = x[2 * gg + 1] = pack_half2(hi, y - hi);
@@ -587,16 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
       if (!warp_wait_all(v_empty(b2), ((j >> 1) & 1) ^ 1, err, kErrWaitEmpty, abort_flag)) break;
       const uint8_t* raw = smem + L::kRawAt + sl * L::kRawTile + w4 * B::kBytes;
       uint8_t* tab = smem + L::kTab + w4 * (4 * NG * 32);  // [tig][group][f] (s pair, m + 8 s pair) of the warp's block
-      const Token t = token_of(a, vis, (t_begin + j) * 4 + w4, tok_of, i_first, i_last);
+      const bool seen = seen_token(a, vis, from, (t_begin + j) * 4 + w4, tok_of);
 #pragma unroll
       for (int gg = 0; gg < NG; ++gg) {
         const uint32_t sm = reinterpret_cast<const uint32_t*>(raw + B::kVs)[tok_of * NG + gg];
         float sc = q4_scale(sm), mid = fmaf(sc, 8.f, q4_min(sm));
-        // poisoned and seen by some rows only: those become NaN in the softmax
-        const bool bad = t.some && !t.every && sc != sc;
-        if (!t.some || bad) sc = mid = 0.f;
-        const uint32_t word = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) poison[((j & 3) * NG + gg) * 4 + w4] = word;
+        if (!seen) sc = mid = 0.f;
         __half* x = reinterpret_cast<__half*>(tab) + ((tig_of * NG + gg) * 4 + f_of) * 4 + half_of;
         x[0] = __float2half_rn(sc * norm);
         x[2] = __float2half_rn(mid * norm);

@@ -98,4 +98,23 @@ __device__ __forceinline__ int q4_v_word(int d, int tig) {
   return (j >> 2) * 512 + ((d & 7) * 4 + tig) * 16 + (j & 3) * 4;
 }
 
+// E consecutive channels from ch0 (a multiple of E, E divides 8) of token t of a block.
+template <int D, int E>
+__device__ __forceinline__ void q4_token(const uint8_t* blk, int t, int ch0, float (&k)[E], float (&v)[E]) {
+  using B = Q4Block<D>;
+  auto word = [&](int at) { return __ldg(reinterpret_cast<const uint32_t*>(blk + at)); };
+  const int c8 = ch0 >> 3, gg = ch0 / kQ4Group;
+  const uint32_t ks = word(B::kKs + (t * B::kGroups + gg) * 4), vs = word(B::kVs + (t * B::kGroups + gg) * 4);
+  const uint32_t kw = word(t * B::kRow + ((c8 & 7) >> 1) * (D / 8) + ((c8 >> 3) * 2 + (c8 & 1)) * 4);
+  const int tig = (t & 7) >> 1, n = q4_k_channel((t >> 4) * 2 + (t >> 3 & 1), t & 1);  // the token's nibble in V's words
+  auto value = [](uint32_t w, int nibble, uint32_t sm) {
+    return fmaf((float)(__funnelshift_r(w, w, 2) >> (4 * nibble) & 15u), q4_scale(sm), q4_min(sm));
+  };
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    k[e] = value(kw, (ch0 & 7) + e, ks);
+    v[e] = value(word(B::kV + q4_v_word(ch0 + e, tig)), n, vs);
+  }
+}
+
 }  // namespace skv

@@ -27,4 +27,19 @@ __device__ __forceinline__ Visible visible_of(const WindowArgs& a, int s) {
   return x;
 }
 
+// A tile of query rows takes the cache tokens that all of its rows see: those below
+// n_sink and those from `tile_from` (the window of the tile's last text token) on.  Its
+// other rows also see tokens before that, from `row_from` on; the kernels join
+// those row by row with the text tokens, since what a tile keeps for all of its
+// rows (references and exponents of keys and values) must not depend on a token
+// that the mask hides from one of them.
+__device__ __forceinline__ int row_from(const WindowArgs& a, int L, int i) {
+  if (!a.window) return 0;
+  const long long from = (long long)L + i - a.window + 1;
+  return from <= 0 ? 0 : from >= L ? L : (int)from;
+}
+__device__ __forceinline__ int tile_from(const WindowArgs& a, int L, int i_last) { return row_from(a, L, i_last); }
+// The last text token of row tile `tile` (R rows, G a text token).
+__device__ __forceinline__ int tile_last(int tile, int rows, int R, int G) { return (min((tile + 1) * rows, R) - 1) / G; }
+
 }  // namespace skv

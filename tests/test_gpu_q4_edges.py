@@ -103,3 +103,57 @@ def test_sink_window_prefill_of_infinite_keys(sign, d, dtype):
     assert torch.isnan(out[0, sees, 1:]).all() and torch.isnan(lse[0, 1:, sees]).all()
     for rows in (slice(0, at), slice(at + window, n)):
         check_attention(out[0, rows], lse[0][:, rows], part_of(clean, rows), dtype, P_PREFILL[dtype])
+
+
+# -------------------------------------------- tokens that only some rows see
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,Hq", [(3, 7), (2, 7), (30, 7), (70, 2)])
+@pytest.mark.parametrize("which", ["v", "k", "both"])
+@pytest.mark.parametrize("size", [1e6, 1e30])
+def test_decode_hidden_finite_values_have_no_influence(size, which, n, Hq, dtype):
+    """A large key or value that the window hides from all but the first text
+    tokens: their rows see it, the others keep the precision of what they see."""
+    S, Hkv, d, L, window = 1, 1, 128, 300, 120
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    at = L - window + 1                      # text token 0 alone sees it
+    if which != "k":
+        pv[:, at] *= size
+    if which != "v":
+        pk[:, at] *= size
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L, window=window, n_sink=2)
+    want = decode_reference(q[0], k[0], v[0], pk[0], pv[0], window, 2)
+    check_attention(out[0, 1:], lse[0][:, 1:], part_of(want, slice(1, n)), dtype, P_DECODE[dtype])
+    check_attention(out[0], lse[0], want, dtype, P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L,n,window,n_sink", [
+    (100, 9, 1, 0), (100, 9, 4, 0), (100, 9, 9, 3), (64, 40, 37, 0), (64, 40, 70, 64), (33, 33, 33, 33),
+    (1, 5, 3, 0), (2000, 6, 1500, 1), (2000, 60, 31, 500), (0, 8, 3, 0)])
+def test_decode_at_the_edge_of_the_window(L, n, window, n_sink, d, dtype):
+    """Every position at which a window's edge can stand among cached tokens, first
+    tokens and text tokens, with one, two and seven heads a KV head, over lengths on
+    the host and on the device."""
+    S, Hkv = 2, 2
+    for G in (1, 2, 7):
+        pk, pv = tokens(1, S, max(L, 1), Hkv, d, dtype)
+        k, v = tokens(2, S, n, Hkv, d, dtype)
+        q, _ = tokens(3, S, n, G * Hkv, d, dtype, loud=False)
+        c = _skv().Q4Cache(Hkv, d, L + 7, n_streams=S)
+        c.data.fill_(255)
+        if L:
+            c.append(pk.cuda(), pv.cuda(), 0)
+        lens = [L, L // 2]
+        at = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for where, of in ((L, [L, L]), (at, lens)):
+            out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), where, window=window, n_sink=n_sink)
+            for s in range(S):
+                want = decode_reference(q[s], k[s], v[s], pk[s, :of[s]], pv[s, :of[s]], window, n_sink)
+                check_attention(out[s], lse[s], want, dtype, P_DECODE[dtype])
