@@ -286,8 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     fence_proxy_async();
   }
   __syncthreads();
-  // exponents that bring it into [2^12, 2^13)
-  const int eK = min(max((int)(tops[0] >> 23) - 127 - 12, -100), 100), eV = min(max((int)(tops[1] >> 23) - 127 - 12, -100), 100);
+  // exponents that bring it into [2^12, 2^13) (116 where the bound itself overflows;
+  // the values, below 2^128, are below 2^12 then)
+  const int eK = max((int)(tops[0] >> 23) - 127 - 12, -100), eV = max((int)(tops[1] >> 23) - 127 - 12, -100);
   auto col_s = [](int x) { return (uint32_t)(x * 128); };
   constexpr uint32_t kColO = 256, kColQx = 384;
 
@@ -358,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     float m_used = -INFINITY, l = 0.f, c = 0.f;
     bool ok = n > 0;
     if (ok) {
-      c = reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK);
+      // (finite: the largest queries and keys need not meet in a channel)
+      c = fminf(reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK), 0x1.fffffep127f);
       if (half == 0) {
         // the row's sums of q for the product of depth 16: per group hi hi lo lo,
         // against m + 8 s as hi lo hi lo (a factor of 4 moved over: fp16's range)

@@ -157,3 +157,33 @@ def test_decode_at_the_edge_of_the_window(L, n, window, n_sink, d, dtype):
             for s in range(S):
                 want = decode_reference(q[s], k[s], v[s], pk[s, :of[s]], pv[s, :of[s]], window, n_sink)
                 check_attention(out[s], lse[s], want, dtype, P_DECODE[dtype])
+
+
+# ---------------------------------------------------------- the largest floats
+LARGE = [
+    # Hq (of one KV head), n, L: 8 rows, 14 rows, 112, 280
+    (7, 1, 300), (7, 1, 1700), (7, 2, 900), (7, 16, 900), (7, 40, 900), (40, 1, 900)]
+
+
+def decode_values(size, Hq, n, L, dtype, flat):
+    S, Hkv, d = 1, 1, 128
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    if flat:
+        pv, v = pv.abs() + 4, torch.full_like(v, 6.0)
+    pv, v = pv * size, v * size
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
+    check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0], pv[0], 0, 0), dtype, P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n,L", LARGE)
+@pytest.mark.parametrize("size", [2.0 ** 116, 2.0 ** -100])
+def test_decode_of_large_and_tiny_values(size, Hq, n, L, dtype):
+    """Values of one sign or of both beyond what one scale of fp16 numbers would hold."""
+    for flat in (False, True):
+        decode_values(size, Hq, n, L, dtype, flat)
