@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
   constexpr int kStride = D + 4;      // padded row of the partials in shared memory
   constexpr bool kAlone = kShare == kOwn;
   constexpr bool kCentred = NS == 2;  // codes as c - 8, else as subnormals
-  // S^T and O^T are in units of kUnit: with Q (P s) 16 times larger where the code is c 2^-22
-  constexpr float kCodeNear = 0x1p-18f, kCodeFar = 0x1p-22f, kUnit = kCentred ? 1.f : kCodeNear;
+  // with Q (P s) 16 times larger where the code is c 2^-22
+  constexpr float kCodeNear = 0x1p-18f, kCodeFar = 0x1p-22f, kUnit = 0x1p-18f;
   extern __shared__ __align__(16) uint8_t smem[];
   const WindowArgs& a = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     // ---- Q fragments, per-row scale and group sums
     uint32_t qf[NT][NS][MT][2];
     float qsum[NT][NG][2], rs[NT][2];
+    uint32_t huge_rows = 0;  // bit 2 nt + e
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float top = 0.f;
@@ -388,9 +389,14 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // largest element into [2^10, 2^11); 1 for a zero row or one with an infinity
       int ex = (int)(__float_as_uint(top) >> 23);
-      ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, 12);
+      // (the least exponent keeps 2^(264 - ex), or 16 times it, finite)
+      ex = ex == 0 && top == 0.f ? 137 : ex == 255 ? 137 : max(ex, kCentred ? 12 : 16);
       const float up = __uint_as_float((uint32_t)(264 - ex) << 23);  // 2^(10 - (ex - 127))
-      const float down = __uint_as_float((uint32_t)(ex - 10) << 23);
+      // S is summed in units of 2^18, which leave it below the largest key (q is below
+      // 2^11, 128 channels); the row factor 2^(ex - 137) takes that up, or, where q is
+      // so large that it could overflow, S itself afterwards
+      const bool huge = ex >= 200;
+      const float down = __uint_as_float((uint32_t)(huge ? ex - 10 : ex + 8) << 23);
       float sum[NG];
 #pragma unroll
       for (int gg = 0; gg < NG; ++gg) sum[gg] = 0.f;
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
           qf[nt][0][2 * w + (f >> 1)][f & 1] = half2_bits(hi);
           if (kCentred) {
             qf[nt][NS - 1][2 * w + (f >> 1)][f & 1] = half2_bits(__floats2half2_rn(x0 - h.x, x1 - h.y));
-            sum[w >> 1] += x0 + x1;
+            sum[w >> 1] += (x0 + x1) * kUnit;
           } else {
             sum[w >> 1] += (h.x + h.y) * (f == 1 || f == 2 ? kCodeFar : kCodeNear);
           }
@@ -422,6 +428,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 #pragma unroll
         for (int gg = 0; gg < NG; ++gg) qsum[nt][gg][e] = __shfl_sync(0xffffffffu, sum[gg], from);
         rs[nt][e] = __shfl_sync(0xffffffffu, down, from) * a.scale_log2;
+        if (__shfl_sync(0xffffffffu, huge, from)) huge_rows |= 1u << (2 * nt + e);
       }
     }
 
@@ -456,13 +463,14 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
     }
 
     const int from = tile_from(a, vis.L, i_last);
+    const bool any_huge = __any_sync(0xffffffffu, huge_rows != 0);
     for (int v = v0 + warp; ok && v < v1; v += kWarps, ++done) {
       const int stage = done % kStages;
       const uint32_t bar = bars + 8u * stage, parity = (done / kStages) & 1;
       if (!(ok = tc::warp_wait_all(bar, parity, &g_err, tc::kErrWaitLoad, abort_flag))) break;
       const uint8_t* blk = ring + stage * B::kBytes;
       const int t0 = vis.block(v) * kQ4Tokens;
-      const bool full = t0 + kQ4Tokens <= vis.L && (t0 >= from || t0 + kQ4Tokens <= a.n_sink);
+      const bool plain = !any_huge && t0 + kQ4Tokens <= vis.L && (t0 >= from || t0 + kQ4Tokens <= a.n_sink);
       // ---- S^T = K Q^T, 16 tokens at a time; t rs = logits in log2 units
       float t[NT][2][4];
 #pragma unroll
@@ -515,14 +523,8 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float sum = gg == 0 ? mid * qsum[nt][0][e] : fmaf(mid, qsum[nt][gg][e], t[nt][kt][hh * 2 + e]);
-                t[nt][kt][hh * 2 + e] = fmaf(sc, acc[nt][gg][hh * 2 + e], sum);
+                t[nt][kt][hh * 2 + e] = fmaf(sc, kCentred ? acc[nt][gg][hh * 2 + e] * kUnit : acc[nt][gg][hh * 2 + e], sum);
               }
-          }
-          if (!kCentred) {  // (in Q's factor or the scales 2^18 could overflow)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) t[nt][kt][hh * 2 + e] *= 1.f / kUnit;
           }
         }
       }
@@ -541,8 +543,16 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
             mv[kt][hh][gg] = fmaf(sv[kt][hh][gg], 8.f, q4_min(sm));
           }
         }
-      // ---- masks: hidden tokens get a logit of -inf and a V scale of 0
-      if (!full) {
+      // ---- masks: hidden tokens get a logit of -inf and a V scale of 0 (and the rows of
+      // large queries their 2^18, here rather than in a branch of its own: 1 us of 53)
+      if (!plain) {
+        if (any_huge) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (huge_rows >> (2 * nt + (c & 1)) & 1) t[nt][c >> 2][c & 3] *= 1.f / kUnit;
+        }
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll

@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
   }
   __syncthreads();
   // exponents that bring it into [2^12, 2^13) (116 where the bound itself overflows;
-  // the values, below 2^128, are below 2^12 then)
-  const int eK = max((int)(tops[0] >> 23) - 127 - 12, -100), eV = max((int)(tops[1] >> 23) - 127 - 12, -100);
+  // the values, below 2^128, are below 2^12 then), as far down as exp2i reaches
+  const int eK = max((int)(tops[0] >> 23) - 127 - 12, -126), eV = max((int)(tops[1] >> 23) - 127 - 12, kPShift - 126);
   auto col_s = [](int x) { return (uint32_t)(x * 128); };
   constexpr uint32_t kColO = 256, kColQx = 384;
 

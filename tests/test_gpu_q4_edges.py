@@ -165,6 +165,25 @@ LARGE = [
     (7, 1, 300), (7, 1, 1700), (7, 2, 900), (7, 16, 900), (7, 40, 900), (40, 1, 900)]
 
 
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n,L", LARGE)
+def test_decode_of_large_keys(Hq, n, L, dtype):
+    """Keys of up to 2^124 that meet queries as small, and the reverse: logits of
+    ordinary size."""
+    S, Hkv, d = 1, 1, 128
+    for e in (120, -100, -122):
+        pk, pv = tokens(1, S, L, Hkv, d, dtype)
+        k, v = tokens(2, S, n, Hkv, d, dtype)
+        q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+        pk, k, q = pk * 2.0 ** e, k * 2.0 ** e, q * 2.0 ** -e
+        c = _skv().Q4Cache(Hkv, d, L)
+        c.append(pk.cuda(), pv.cuda(), 0)
+        out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
+        check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0], pv[0], 0, 0), dtype,
+                        P_DECODE[dtype])
+
+
 def decode_values(size, Hq, n, L, dtype, flat):
     S, Hkv, d = 1, 1, 128
     pk, pv = tokens(1, S, L, Hkv, d, dtype)
