@@ -392,6 +392,9 @@ int statekv_q4_read(const void* cache, int n_streams, int Hkv, int d, int capaci
  * largest so far of a row's weights and of the visible scales: 2^-11 of it, and
  * what is below 2^-29 of the largest counts as 0.  float32 calls hold it in two
  * such parts.
+ * A row of finite inputs whose weighted sum of values leaves float32's range
+ * (values above some 2^128 over the number of tokens) is computed a second time,
+ * slowly; so is one that sees a NaN or an infinity among the text values.
  * workspace: device memory of at least statekv_q4_decode_workspace bytes
  * (16-byte aligned) that no other work uses until this call's has run; its
  * contents do not matter.

@@ -71,6 +71,11 @@ constexpr float kRaise = 6.f;   // log2 headroom of the lazy row maximum
 constexpr float kMinR = 0x1p-118f;  // least V reference (kPScale / R stays finite)
 constexpr float kPScale = 512.f;    // P s <= 2^6 * 512 < 65504
 
+// Sums of weights times values can overflow where their quotient, a mean of the
+// values, does not (values above 2^128 over the tokens' number): a row whose result is
+// not finite is taken again with values in units of 1 / kLess.
+constexpr float kLess = 0x1p-40f;
+
 constexpr int kOwnText = 32;  // most text tokens of a call whose thread blocks join them one by one
 
 __device__ int g_err;  // first error of the ring's waits of all calls on a device
@@ -210,20 +215,21 @@ struct RowSum {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
   }
-  __device__ __forceinline__ void join(float m2, float l2, const float (&v)[E]) {  // acc += v (weights relative to 2^m2)
+  __device__ __forceinline__ void join(float m2, float l2, const float (&v)[E], float unit = 1.f) {  // acc += unit v (weights relative to 2^m2)
     const float nm = fmaxf(m, m2);
     const float ref = nm == -INFINITY ? 0.f : nm;
     const float f1 = tc::ex2_approx(m - ref), f2 = tc::ex2_approx(m2 - ref);
     l = l * f1 + l2 * f2;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + v[e] * f2;
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * f1 + v[e] * (f2 * unit);
     m = nm;
   }
 };
 // What the row (text token i, head h) sees beside the cache tokens of its whole tile:
 // cache tokens behind its own window's edge and before that of the tile's last
 // text token, and the text tokens; of both the ones first, first + step, ...
-template <typename T, int D>
+// kAll: all that it sees, with values in units of 1 / kLess.
+template <typename T, int D, bool kAll = false>
 __device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int h, int g, int i, int i_last, int first,
                                          int step, RowSum<D / 32>& sum) {
   constexpr int E = D / 32;
@@ -251,19 +257,21 @@ __device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int 
 #pragma unroll
       for (int b = 0; b < N; ++b) {
         if (t[b] != t[b]) sum.l = t[b];  // a NaN logit makes the row NaN
-        sum.join(t[b], 1.f, v[b]);
+        sum.join(t[b], 1.f, v[b], kAll ? kLess : 1.f);
       }
       j += N * step;
     };
     while (j < end - 3 * step) some(std::integral_constant<int, 4>());
     while (j < end) some(std::integral_constant<int, 1>());
   };
-  if (a.window) {
-    const int end = tile_from(a, L, i_last);
+  if (a.window || kAll) {
+    const int end = kAll ? L : tile_from(a, L, i_last), sinks = a.window ? min(a.n_sink, end) : 0;
     const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * Q4Block<D>::kBytes;
-    run(max(row_from(a, L, i), min(a.n_sink, end)) + first, end, [&](int j, float (&k)[E], float (&v)[E]) {
+    auto cached = [&](int j, float (&k)[E], float (&v)[E]) {
       q4_token<D, E>(cache + (long long)(j / kQ4Tokens) * Q4Block<D>::kBytes, j % kQ4Tokens, lane * E, k, v);
-    });
+    };
+    if (kAll) run(first, sinks, cached);
+    run(max(row_from(a, L, i), sinks) + first, end, cached);
   }
   auto text = [&](int j, float (&k)[E], float (&v)[E]) {
     const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
@@ -280,12 +288,40 @@ __device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int 
   run(from + first, i + 1, text);
 }
 
+// One row again by a warp, token by token, where its result is not finite in the
+// groups of channels `groups`: slow, and only where sums overflow or inputs hold a
+// NaN or an infinity.  A visible NaN scale explains its group's result, which stands then.
+template <typename T, int D>
+__device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h, int g, int i, uint32_t groups) {
+  using B = Q4Block<D>;
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
+  const int from = row_from(a, L, i);
+  uint32_t nan = 0;
+  for (int j = lane; j < L; j += 32) {
+    if (j < from && j >= a.n_sink) continue;
+    const uint8_t* scales = cache + (long long)(j / kQ4Tokens) * B::kBytes + B::kVs + j % kQ4Tokens * (B::kGroups * 4);
+#pragma unroll
+    for (int gg = 0; gg < B::kGroups; ++gg) {
+      const float sc = q4_scale(__ldg(reinterpret_cast<const uint32_t*>(scales) + gg));
+      if (sc != sc) nan |= 1u << gg;
+    }
+  }
+  if ((groups & ~__reduce_or_sync(0xffffffffu, nan)) == 0) return;
+  RowSum<E> sum;
+  join_own<T, D, true>(a, L, s, h, g, i, i, 0, 1, sum);
+  T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = from_f<T>(sum.acc[e] / sum.l * (1.f / kLess));
+}
+
 // How a call is shared out: over the workers (one length, or lengths on the device),
 // or a thread block alone for each (stream, KV head).
 enum Share { kEven, kRagged, kOwn };
 
 template <typename T, int D, int NT, int NS, Share kShare>
-__global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4AttnArgs p) {
+__global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(const __grid_constant__ Q4AttnArgs p) {
   using B = Q4Block<D>;
   constexpr int kWarps = warps_of<NT, NS>();
   constexpr int NG = B::kGroups;
@@ -763,8 +799,14 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
         for (int e = 0; e < E; ++e) sum.acc[e] = wo[r * kStride + lane * E + e];
         join_own<T, D>(a, vis.L, s, h, g, i, i_last, 0, 1, sum);
         T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+        bool large = false;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = from_f<T>(sum.acc[e] / sum.l);
+        for (int e = 0; e < E; ++e) {
+          large |= !(fabsf(sum.acc[e]) < INFINITY);
+          out[e] = from_f<T>(sum.acc[e] / sum.l);
+        }
+        const unsigned again = __ballot_sync(0xffffffffu, large && sum.l == sum.l);
+        if (again) row_again<T, D>(a, vis.L, s, h, g, i, NG == 1 ? 1u : (again & 0xffffu ? 1u : 0u) | (again >> 16 ? 2u : 0u));
         if (lane == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (sum.m + log2f(sum.l)) * kLn2;
       }
       return;
@@ -781,7 +823,7 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(Q4A
 // own running maximum; then the eight are joined in order.
 constexpr int kMergeWarps = 8;
 template <typename T, int D, bool kRaggedLengths>
-__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const __grid_constant__ Q4AttnArgs p) {
   constexpr int E = D / 32;  // channels per lane
   __shared__ float s_acc[kMergeWarps][D];
   __shared__ float s_ml[kMergeWarps][2];
@@ -844,6 +886,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, s_ml[w][0]);
   const float ref = mx == -INFINITY ? 0.f : mx;
+  bool large = false;
   for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) {
     float o = 0.f, ls = 0.f;
 #pragma unroll
@@ -854,6 +897,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(Q4AttnArgs p
     }
     static_cast<T*>(a.out)[(((long long)s * a.n + i) * a.Hq + h) * D + d] = from_f<T>(o / ls);
     if (d == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (mx + log2f(ls)) * kLn2;
+    large = !(fabsf(o) < INFINITY) && ls == ls;
+  }
+  if (__syncthreads_or(large)) {
+    const uint32_t first = __syncthreads_or(large && warp < 2), second = __syncthreads_or(large && warp >= 2);
+    if (warp == 0) row_again<T, D>(a, vis.L, s, h, g, i, (first ? 1u : 0u) | (second ? 2u : 0u));
   }
 }
 

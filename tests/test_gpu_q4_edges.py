@@ -206,3 +206,57 @@ def test_decode_of_large_and_tiny_values(size, Hq, n, L, dtype):
     """Values of one sign or of both beyond what one scale of fp16 numbers would hold."""
     for flat in (False, True):
         decode_values(size, Hq, n, L, dtype, flat)
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n,L", LARGE)
+def test_decode_of_values_whose_sum_overflows(Hq, n, L, dtype):
+    """Values next to the largest float, whose sum over the tokens would not fit: the
+    result, their mean, does."""
+    for flat in (False, True):
+        decode_values(2.0 ** 124, Hq, n, L, dtype, flat)
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_decode_of_large_text_values(n, dtype):
+    """The text tokens' own values next to the largest float, an ordinary cache."""
+    S, Hq, Hkv, d, L = 1, 7, 1, 128, 200
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    k[:] = 0
+    v = (v.abs() + 4) * 2.0 ** 124
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    for past in (L, 0):
+        out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), past)
+        check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0, :past], pv[0, :past], 0, 0), dtype,
+                        P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,L", [(1, 300), (1, 1700), (40, 900)])
+def test_decode_of_large_and_poisoned_values_in_a_window(n, L, dtype):
+    """Values whose sum overflows beside a group of 64 channels that holds a NaN: the
+    rows that see it are NaN in that group alone."""
+    S, Hq, Hkv, d, window, n_sink = 1, 7, 1, 128, 200, 4
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    pv, v = (pv.abs() + 4) * 2.0 ** 124, (v.abs() + 4) * 2.0 ** 124
+    want = decode_reference(q[0], k[0], v[0], pk[0], pv[0], window, n_sink)
+    sees = 25                                # rows below it see the token
+    at = L - window + sees
+    pv[0, at, 0, 70] = float("nan")
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L, window=window, n_sink=n_sink)
+    rows = min(n, sees)
+    assert torch.isnan(out[0, :rows, :, 64:]).all()
+    got = out.clone()
+    got[0, :rows, :, 64:] = torch.from_numpy(want[0][:rows, :, 64:]).to(out)
+    check_attention(got[0], lse[0], want, dtype, P_DECODE[dtype])
