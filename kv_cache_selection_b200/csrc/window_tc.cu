@@ -81,25 +81,57 @@ __device__ __forceinline__ void after_wait(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// One row again, from its visible tokens alone; a warp, lane = D/32 channels.
+// One row again, from its visible tokens alone, by a warp.  The row's result is in
+// `out` already; where all of it that is not finite comes from a visible value that is
+// a NaN or an infinity, it stands, so that inputs with NaNs cost one pass over the
+// values at most.  The row's lse is right as it is.
 template <int D>
 __device__ __noinline__ void row_again(const WindowArgs& a, int s, int h, int i) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32;  // channels of a lane
+  using T = __nv_bfloat16;
   const int lane = threadIdx.x & 31, g = h / (a.Hq / a.Hkv);
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+  const long long row = (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
+  const long long kv0 = ((long long)s * a.n * a.Hkv + g) * D + lane * E, step = (long long)a.Hkv * D;
+  T* out = static_cast<T*>(a.out) + row;
+  const T* k = static_cast<const T*>(a.k) + kv0;
+  const T* v = static_cast<const T*>(a.v) + kv0;
+  // tokens [0, sinks) and [first, i]
+  const int first = max(0, i - a.window + 1), sinks = min(a.n_sink, first);
+  const int count = sinks + i + 1 - first;
+  auto token = [&](int x) { return x < sinks ? x : x - sinks + first; };
+
+  __syncwarp();  // (lanes of the warp wrote `out`)
+  bool bad[E], some = true;
+#pragma unroll
+  for (int e = 0; e < E; ++e) bad[e] = !(fabsf(to_f(out[e])) < INFINITY);
+  for (int x0 = 0; some && x0 < count; x0 += 8) {
+    float y[8][E];
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[b][e] = to_f(v[token(min(x0 + b, count - 1)) * step + e]);
+    some = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+#pragma unroll
+      for (int b = 0; b < 8; ++b) bad[e] &= fabsf(y[b][e]) < INFINITY;
+      some |= bad[e];
+    }
+    some = __any_sync(0xffffffffu, some);
+  }
+  if (!some) return;
+
   float qv[E], o[E], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    qv[e] = to_f(q[e]);
+    qv[e] = to_f(static_cast<const T*>(a.q)[row + e]);
     o[e] = 0.f;
   }
-  const int first = max(0, i - a.window + 1);
-  for (int j = 0; j <= i; ++j) {
-    if (j >= a.n_sink && j < first) j = first;
-    const long long at = (((long long)s * a.n + j) * a.Hkv + g) * D + lane * E;
+  for (int x = 0; x < count; ++x) {
+    const long long at = token(x) * step;
     float t = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) t = fmaf(qv[e], to_f(static_cast<const __nv_bfloat16*>(a.k)[at + e]), t);
+    for (int e = 0; e < E; ++e) t = fmaf(qv[e], to_f(k[at + e]), t);
 #pragma unroll
     for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
     t *= a.scale_log2;
@@ -108,19 +140,17 @@ __device__ __noinline__ void row_again(const WindowArgs& a, int s, int h, int i)
     const float f = ex2_approx(m - ref), p = ex2_approx(t - ref);
     l = l * f + p;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f(static_cast<const __nv_bfloat16*>(a.v)[at + e]);
+    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f(v[at + e]);
     m = nm;
   }
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f<__nv_bfloat16>(o[e] / l);
-  if (a.lse && lane == 0) a.lse[((long long)s * a.Hq + h) * a.n + i] = (m + __log2f(l)) * kLn2;
+  for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] / l);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, WindowArgs a, int n_pairs) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowArgs a, int n_pairs) {
   using L = Smem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -436,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       const float inv = 1.f / l;
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D;
-      bool bad = !(fabsf(inv) < INFINITY);
+      bool bad = false;
 #pragma unroll
       for (int c0 = 0; c0 < D / 32; ++c0) {
         uint32_t v[32];
@@ -456,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (i < a.n && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (m_used + __log2f(l)) * kLn2;
-      unsigned again = __ballot_sync(0xffffffffu, bad && i < a.n);
+      // (a NaN in the sum of weights: a visible logit was one, so the row is NaN)
+      unsigned again = __ballot_sync(0xffffffffu, bad && l == l && i < a.n);
       __syncwarp();
       while (again) {
         const int b = __ffs(again) - 1;

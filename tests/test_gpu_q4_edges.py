@@ -105,6 +105,41 @@ def test_sink_window_prefill_of_infinite_keys(sign, d, dtype):
         check_attention(out[0, rows], lse[0][:, rows], part_of(clean, rows), dtype, P_PREFILL[dtype])
 
 
+@cuda
+@pytest.mark.parametrize("where", ["q", "k", "v", "v[0]"])
+def test_sink_window_prefill_of_nan_inputs_costs_no_more(where):
+    """Inputs full of NaNs (or one NaN value in every 100th token) take the time of
+    finite ones and no multiple of it: ten times as much is allowed where rows that
+    are recomputed one by one take some hundred times as much."""
+    n, Hq, Hkv, d, window = 4096, 4, 1, 64, 1024
+    k, v = tokens(1, 1, n, Hkv, d, "bf16")
+    q, _ = tokens(2, 1, n, Hq, d, "bf16", loud=False)
+    ins = {"q": q.cuda(), "k": k.cuda(), "v": v.cuda()}
+
+    def ms():
+        call = lambda: _skv().sink_window_prefill(ins["q"], ins["k"], ins["v"], window, n_sink=4)
+        out, _ = call()
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record(), call(), b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best, out
+
+    clean, _ = ms()
+    if where == "v[0]":
+        ins["v"][:, ::100, :, 0] = float("nan")
+    else:
+        ins[where][:] = float("nan")
+    odd, out = ms()
+    rows = out[0, 100:, :, :1] if where == "v[0]" else out
+    assert torch.isnan(rows).all()
+    if where == "v[0]":
+        assert torch.isfinite(out[..., 1:]).all()
+    assert odd <= 10 * clean, f"{odd:.3f} ms against {clean:.3f}"
+
+
 # -------------------------------------------- tokens that only some rows see
 @cuda
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
