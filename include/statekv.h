@@ -421,9 +421,14 @@ int statekv_q4_status(int* code);
  *   q [n_tokens][Hq][d], k,v [n_tokens][Hkv][d], out [n_tokens][Hq][d] (device,
  *   dtype); lse [Hq][n_tokens] float32 natural-log (device) or NULL.
  * window >= 1, n_sink >= 0.  Work grows with n_tokens x (window + n_sink).  A
- * key or value the mask hides takes no part, whatever it holds (a bf16 row that
- * shares a tile of 128 keys with a hidden NaN or infinity is computed a second
- * time, slowly, and may differ in its last bits).  No memory is allocated.
+ * key or value the mask hides takes no part, whatever it holds.  Some rows are
+ * computed a second time, slowly: in bf16 those that share a tile of 128 keys with
+ * a hidden NaN or infinity (they may differ in their last bits), in either type
+ * those whose weighted sum of values leaves float32's range though the result, a
+ * mean, does not (values above some 2^128 over the number of tokens).
+ * bf16 calls round each weight to bf16 before it meets its value (2^-8 of the
+ * weight at most; the sum of the weights is float32); float32 calls keep
+ * float32's precision.  No memory is allocated.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int sink_window_prefill(const void* q, const void* k, const void* v, int n_tokens, int Hq, int Hkv,
                         int d, int dtype, int window, int n_sink, void* out, float* lse,

@@ -30,6 +30,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "window_row.cuh"
 
 namespace skv {
 namespace {
@@ -78,10 +79,12 @@ __device__ __forceinline__ void split(float x, uint32_t& hi, uint32_t& lo) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArgs a, int n_tiles) {
+__global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(const __grid_constant__ WindowArgs a, int n_tiles) {
   using L = Tile<D>;
   constexpr int KT = L::kKeys, NT = KT / 8, KP = D / 16, VQ = D / 32;
   extern __shared__ __align__(16) float smem[];
+  // channels of this lane's rows (bits 8 c + 4 b + i) that met a value not finite
+  __shared__ uint32_t seen[2][kThreads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   // unit -> (stream, row tile, head): the heads that share keys run side by side
   long long u = blockIdx.x;
@@ -133,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
   for (int e = 0; e < 2; ++e) {
     m[e] = -INFINITY;
     l[e] = 0.f;
+    seen[e][threadIdx.x] = 0u;
   }
 
   for (int j = 0; j < nk; ++j) {
@@ -151,6 +155,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
       odd |= !(fabsf(y.x) < kBig) || !(fabsf(y.y) < kBig) || !(fabsf(y.z) < kBig) || !(fabsf(y.w) < kBig);
     }
     const bool careful = __syncthreads_or(odd);  // (the tile is there, the one before has been read)
+    bool big = false;  // a key that is infinite, or too large to be rounded
+    if (careful) {
+#pragma unroll
+      for (int e = threadIdx.x; e < KT * D / 4; e += kThreads) {
+        const float4 x = *reinterpret_cast<const float4*>(kt + e / (D / 4) * L::kKStride + e % (D / 4) * 4);
+        big |= fabsf(x.x) >= kBig || fabsf(x.y) >= kBig || fabsf(x.z) >= kBig || fabsf(x.w) >= kBig;
+      }
+      big = __syncthreads_or(big);
+    }
     if (j + 1 < nk) load(j + 1);
     // a warp whose rows see nothing of the tile leaves it out
     const int w0 = i0 + warp * 16;
@@ -184,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
           if (kAny) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (!(fabsf(y[i]) < kBig)) y[i] = 0.f;
+              if (fabsf(y[i]) >= kBig) y[i] = 0.f;  // (a NaN stays: the logit is one)
           }
           uint32_t ya[2][2], yb[2][2];
           split<false>(y[0], ya[0][0], ya[1][0]);
@@ -199,21 +212,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
         }
       }
     };
-    if (!careful) {
-      scores(std::false_type());
-    } else {
+    if (careful) {
       scores(std::true_type());
       // what was 0 in the products, times q as it is: in parts an infinite key would
       // meet q's low part, which is 0 or of the other sign as often as not
 #pragma unroll 1
-      for (int x = 0; x < 2 * NT; ++x) {  // this lane's keys
+      for (int x = 0; big && x < 2 * NT; ++x) {  // this lane's keys
         const float* row = kt + ((x >> 1) * 8 + tig * 2 + (x & 1)) * L::kKStride;
         const float* q0 = smem + L::kQ + (warp * 16 + gid) * L::kKStride;
         float add[2] = {0.f, 0.f};
 #pragma unroll 1
         for (int c = 0; c < D; ++c) {
           const float y = row[c];
-          if (fabsf(y) < kBig) continue;
+          if (!(fabsf(y) >= kBig)) continue;
           add[0] = fmaf(q0[c], y, add[0]);
           add[1] = fmaf(q0[8 * L::kKStride + c], y, add[1]);
         }
@@ -226,6 +237,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
               sc[t][2 + b] += add[1];
             }
       }
+    } else {
+      scores(std::false_type());
     }
 
     // ---- softmax: element e of tile t is row r0 + 8 (e/2), key 8 t + 2 tig + e%2
@@ -317,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
     } else {
       values(std::true_type());
       // what was 0 in the products, for the rows that see it
+      uint32_t met[2] = {0u, 0u};
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll 1
@@ -332,12 +346,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
               for (int b = 0; b < 2; ++b) {
                 const float y = row[c * 32 + b * 4 + i];
                 if (fabsf(y) < kBig) continue;
-                if (__float_as_uint(p0) != 0x80000000u) o[c][i][b] = fmaf(p0, y, o[c][i][b]);
-                if (__float_as_uint(p1) != 0x80000000u) o[c][i][2 + b] = fmaf(p1, y, o[c][i][2 + b]);
+                const uint32_t bit = fabsf(y) < INFINITY ? 0u : 1u << (c * 8 + b * 4 + i);
+                if (__float_as_uint(p0) != 0x80000000u) {
+                  o[c][i][b] = fmaf(p0, y, o[c][i][b]);
+                  met[0] |= bit;
+                }
+                if (__float_as_uint(p1) != 0x80000000u) {
+                  o[c][i][2 + b] = fmaf(p1, y, o[c][i][2 + b]);
+                  met[1] |= bit;
+                }
               }
         }
+      seen[0][threadIdx.x] |= met[0];
+      seen[1][threadIdx.x] |= met[1];
     }
   }
+  uint32_t bad[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int i = r0 + 8 * e;
@@ -350,11 +374,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) window_f32_kernel(WindowArg
 #pragma unroll
     for (int c = 0; c < VQ; ++c)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-        *reinterpret_cast<float4*>(out + c * 32 + b * 4) =
-            make_float4(o[c][0][2 * e + b] * inv, o[c][1][2 * e + b] * inv, o[c][2][2 * e + b] * inv, o[c][3][2 * e + b] * inv);
+      for (int b = 0; b < 2; ++b) {
+        const float4 y = make_float4(o[c][0][2 * e + b] * inv, o[c][1][2 * e + b] * inv, o[c][2][2 * e + b] * inv, o[c][3][2 * e + b] * inv);
+        const uint32_t odd = (fabsf(y.x) < INFINITY ? 0u : 1u) | (fabsf(y.y) < INFINITY ? 0u : 2u) |
+                             (fabsf(y.z) < INFINITY ? 0u : 4u) | (fabsf(y.w) < INFINITY ? 0u : 8u);
+        bad[e] |= odd << (c * 8 + b * 4);
+        *reinterpret_cast<float4*>(out + c * 32 + b * 4) = y;
+      }
+    bad[e] = ls == ls ? bad[e] & ~seen[e][threadIdx.x] : 0u;
     if (a.lse && tig == 0) a.lse[((long long)s * a.Hq + h) * a.n + i] = (m[e] + log2f(ls)) * kLn2;
   }
+  // rows that are not finite where their sum of weights and all values they saw are:
+  // sums of values next to the largest float that overflowed
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e)
+    for (unsigned again = __ballot_sync(0xffffffffu, (e ? bad[1] : bad[0]) != 0u); again;) {
+      const int row = (__ffs(again) - 1) >> 2;
+      again &= ~(0xfu << (4 * row));
+      window_row_again<float, D>(a, s, h, i0 + warp * 16 + row + 8 * e);
+    }
 }
 
 template <int D>

@@ -20,10 +20,10 @@
 // product with V (2^-8 of a weight, the precision of V itself); their sum is
 // float32.
 //
-// A hidden value enters P V with weight 0, and 0 x NaN is NaN: a row that ends
-// with a non-finite output is computed again from its visible tokens alone, on
-// the CUDA cores (slow, and only where the inputs hold a NaN or an infinity or
-// the result overflows).
+// A hidden value enters P V with weight 0, and 0 x NaN is NaN, and sums of values next
+// to the largest float overflow: a row that ends with an output that is not finite,
+// though its sum of weights is, goes through window_row_again (slow, and only
+// where the inputs hold a NaN, an infinity or values that large).
 //
 // Measured (B200): 65536 tokens, 28 heads, d = 128, window 4096: 3365 us, 1112
 // TFLOP/s; 4 x 4001 tokens, 14 heads, d = 64, window 1024: 130 us, 396 TFLOP/s.  At
@@ -41,6 +41,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "tc_common.cuh"
+#include "window_row.cuh"
 
 namespace skv {
 namespace {
@@ -79,72 +80,6 @@ struct Smem {
 __device__ __forceinline__ void after_wait(uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-}
-
-// One row again, from its visible tokens alone, by a warp.  The row's result is in
-// `out` already; where all of it that is not finite comes from a visible value that is
-// a NaN or an infinity, it stands, so that inputs with NaNs cost one pass over the
-// values at most.  The row's lse is right as it is.
-template <int D>
-__device__ __noinline__ void row_again(const WindowArgs& a, int s, int h, int i) {
-  constexpr int E = D / 32;  // channels of a lane
-  using T = __nv_bfloat16;
-  const int lane = threadIdx.x & 31, g = h / (a.Hq / a.Hkv);
-  const long long row = (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
-  const long long kv0 = ((long long)s * a.n * a.Hkv + g) * D + lane * E, step = (long long)a.Hkv * D;
-  T* out = static_cast<T*>(a.out) + row;
-  const T* k = static_cast<const T*>(a.k) + kv0;
-  const T* v = static_cast<const T*>(a.v) + kv0;
-  // tokens [0, sinks) and [first, i]
-  const int first = max(0, i - a.window + 1), sinks = min(a.n_sink, first);
-  const int count = sinks + i + 1 - first;
-  auto token = [&](int x) { return x < sinks ? x : x - sinks + first; };
-
-  __syncwarp();  // (lanes of the warp wrote `out`)
-  bool bad[E], some = true;
-#pragma unroll
-  for (int e = 0; e < E; ++e) bad[e] = !(fabsf(to_f(out[e])) < INFINITY);
-  for (int x0 = 0; some && x0 < count; x0 += 8) {
-    float y[8][E];
-#pragma unroll
-    for (int b = 0; b < 8; ++b)
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[b][e] = to_f(v[token(min(x0 + b, count - 1)) * step + e]);
-    some = false;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-#pragma unroll
-      for (int b = 0; b < 8; ++b) bad[e] &= fabsf(y[b][e]) < INFINITY;
-      some |= bad[e];
-    }
-    some = __any_sync(0xffffffffu, some);
-  }
-  if (!some) return;
-
-  float qv[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_f(static_cast<const T*>(a.q)[row + e]);
-    o[e] = 0.f;
-  }
-  for (int x = 0; x < count; ++x) {
-    const long long at = token(x) * step;
-    float t = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) t = fmaf(qv[e], to_f(k[at + e]), t);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-    t *= a.scale_log2;
-    const float nm = fmaxf(m, t);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    const float f = ex2_approx(m - ref), p = ex2_approx(t - ref);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f(v[at + e]);
-    m = nm;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] / l);
 }
 
 template <int D>
@@ -492,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (again) {
         const int b = __ffs(again) - 1;
         again &= again - 1;
-        row_again<D>(a, s, h, iA + x * 128 + quarter * 32 + b);
+        window_row_again<__nv_bfloat16, D>(a, s, h, iA + x * 128 + quarter * 32 + b);
       }
     }
   }

@@ -140,6 +140,38 @@ def test_sink_window_prefill_of_nan_inputs_costs_no_more(where):
     assert odd <= 10 * clean, f"{odd:.3f} ms against {clean:.3f}"
 
 
+@cuda
+@pytest.mark.parametrize("where", ["q", "k", "v", "one"])
+def test_sink_window_prefill_of_nan_inputs_costs_no_more_in_float32(where):
+    """The same in float32, and for a single NaN in one channel."""
+    n, Hq, Hkv, d, window = 4096, 4, 1, 64, 1024
+    k, v = tokens(1, 1, n, Hkv, d, "f32")
+    q, _ = tokens(2, 1, n, Hq, d, "f32", loud=False)
+    ins = {"q": q.cuda(), "k": k.cuda(), "v": v.cuda()}
+
+    def ms():
+        call = lambda: _skv().sink_window_prefill(ins["q"], ins["k"], ins["v"], window, n_sink=4)
+        out, _ = call()
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record(), call(), b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best, out
+
+    clean, _ = ms()
+    if where == "one":
+        ins["v"][0, 2000, 0, 7] = float("nan")
+    else:
+        ins[where][:] = float("nan")
+    odd, out = ms()
+    assert torch.isnan(out[0, 2000:2000 + window, :, 7] if where == "one" else out).all()
+    if where == "one":
+        assert torch.isnan(out).sum() == window * Hq
+    assert odd <= 10 * clean, f"{odd:.3f} ms against {clean:.3f}"
+
+
 # -------------------------------------------- tokens that only some rows see
 @cuda
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -295,3 +327,16 @@ def test_decode_of_large_and_poisoned_values_in_a_window(n, L, dtype):
     got = out.clone()
     got[0, :rows, :, 64:] = torch.from_numpy(want[0][:rows, :, 64:]).to(out)
     check_attention(got[0], lse[0], want, dtype, P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** 120, 2.0 ** 124, 2.0 ** -100])
+def test_sink_window_prefill_of_large_values(size, d, dtype):
+    n, Hq, Hkv, window = 500, 3, 1, 200
+    k, v = tokens(1, 1, n, Hkv, d, dtype)
+    q, _ = tokens(2, 1, n, Hq, d, dtype, loud=False)
+    v = (v.abs() + 4) * size
+    out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)
+    check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, window, 2), dtype, P_PREFILL[dtype])
