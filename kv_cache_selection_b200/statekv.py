@@ -394,8 +394,8 @@ class Q4Cache:
 
     A group of 64 channels of a token's key or value keeps codes 0..15, a scale
     and a smallest value (include/statekv.h has the rounding).  The buffer is a
-    torch tensor, `data` (a new one, unless one is given); every call runs on
-    `stream`, or on the current stream.  Leading [S] dimensions of q, k and v may be left out
+    torch tensor, `data` (a new one, which waits for the current stream, unless one
+    is given); every call runs on `stream`, or on the current stream.  Leading [S] dimensions of q, k and v may be left out
     when n_streams is 1.
     """
 
@@ -406,6 +406,10 @@ class Q4Cache:
         self.Hkv, self.d, self.capacity, self.S = Hkv, d, capacity, n_streams
         if data is None:
             data = torch.zeros(n, dtype=torch.uint8, device="cuda" if device is None else device)
+            if data.is_cuda and not torch.cuda.is_current_stream_capturing():
+                # calls may come on any stream: none may run ahead of the fill, or of
+                # work that still uses the memory (a captured fill is its graph's)
+                torch.cuda.current_stream(data.device).synchronize()
         else:
             _need(data, (n,), torch.uint8, "data")
         self.data = data

@@ -15,7 +15,7 @@ import pytest
 import torch
 
 from oracle import statekv_oracle as O
-from tests.test_gpu_q4 import DT, Want, _skv, check_attention, cuda, reference, same, tokens
+from tests.test_gpu_q4 import DT, Want, _skv, check_attention, cuda, exact_tensor, reference, same, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -340,3 +340,22 @@ def test_sink_window_prefill_of_large_values(size, d, dtype):
     v = (v.abs() + 4) * size
     out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), window, n_sink=2)
     check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, window, 2), dtype, P_PREFILL[dtype])
+
+
+# ------------------------------------------------------------ streams, arguments
+@cuda
+def test_a_new_cache_is_ready_for_any_stream():
+    """A cache made while the current stream is busy, and appended to at once on
+    another: its fill does not come after the tokens."""
+    Hkv, d, n = 2, 64, 500
+    k, v = tokens(1, 1, n, Hkv, d, "bf16")
+    ins = [k.cuda(), v.cuda()]
+    side = torch.cuda.Stream()
+    for cycles in (0, 40_000_000):           # the kernels are loaded, then some 20 ms
+        torch.cuda.synchronize()
+        torch.cuda._sleep(cycles)
+        c = _skv().Q4Cache(Hkv, d, n)
+        c.append(*ins, 0, stream=side)
+    torch.cuda.synchronize()
+    for t, x in zip(c.read(0, n, dtype="f32"), (k, v)):
+        assert same(t.cpu(), exact_tensor(O.q4_held(x), "f32"))
