@@ -128,7 +128,9 @@ int dev_alloc(statekv_t h, void** p, size_t bytes) {
     *p = nullptr;
     return set_err(h, STATEKV_ERR_OOM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
   }
-  e = cudaMemset(*p, 0, bytes);
+  // the fill runs on the legacy stream: wait for it, since the first use may be on a
+  // stream that does not
+  if ((e = cudaMemset(*p, 0, bytes)) == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
   if (e != cudaSuccess) {
     cudaFree(*p);
     *p = nullptr;

@@ -359,3 +359,30 @@ def test_a_new_cache_is_ready_for_any_stream():
     torch.cuda.synchronize()
     for t, x in zip(c.read(0, n, dtype="f32"), (k, v)):
         assert same(t.cpu(), exact_tensor(O.q4_held(x), "f32"))
+
+
+@cuda
+@pytest.mark.parametrize("detailed", ["native", "q4"])
+def test_a_new_handle_is_ready_for_any_stream(detailed):
+    """The same for a handle whose first step, on another stream, allocates its layer:
+    positions (and native keys) that the step appended stay."""
+    Hq, Hkv, d, T, B = 4, 2, 64, 128, 64
+    k, v = tokens(1, 1, T, Hkv, d, "bf16")
+    q, _ = tokens(2, 1, T, Hq, d, "bf16", loud=False)
+    pos = torch.arange(1, T + 1, dtype=torch.int32)
+    ins = [t.cuda() for t in (q[0], k[0], v[0], pos)]
+    side = torch.cuda.Stream()
+    for cycles in (0, 40_000_000):
+        torch.cuda.synchronize()
+        h = _skv().StateKV(Hq, Hkv, d, T, B, 2, detailed=detailed)
+        torch.cuda._sleep(cycles)
+        with torch.cuda.stream(side):
+            h.prefill_frame(0, *ins)
+        torch.cuda.synchronize()
+        D, C = h.get_detailed(0), h.get_compressed(0)
+        assert D["len"] == T and C["len"] == B
+        assert same(D["pos"][0, :T].cpu(), pos)
+        assert (C["pos"][..., :B] > 0).all()
+        if detailed == "native":
+            assert same(D["k"][0, :, :T].cpu(), k[0].transpose(0, 1).contiguous())
+        h.close()
