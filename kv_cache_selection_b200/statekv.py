@@ -357,6 +357,13 @@ def full_causal_prefill(q, k, v, out=None, lse=None, with_lse=True, stream=None)
     return out, lse
 
 
+def _int32(x, name):
+    """x, if the library's 32-bit arguments hold it (ctypes would cut it off)."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}={x} does not fit 32 bits")
+    return x
+
+
 def _on(dev):
     """Makes a tensor's device the current one; returns the device to go back
     to, or -1 where it already was."""
@@ -400,6 +407,8 @@ class Q4Cache:
     """
 
     def __init__(self, Hkv, d, capacity, n_streams=1, device=None, data=None):
+        for x, name in ((Hkv, "Hkv"), (d, "d"), (capacity, "capacity"), (n_streams, "n_streams")):
+            _int32(x, name)
         n = lib.statekv_q4_bytes(n_streams, Hkv, d, capacity)
         if n < 0:
             _check(int(n))
@@ -444,17 +453,17 @@ class Q4Cache:
         if isinstance(at, torch.Tensor):
             self._need_like(at, (self.S,), torch.int32, name)
             return 0, at.data_ptr()
-        return int(at), None
+        return _int32(int(at), name), None
 
     def append(self, k, v, start, stream=None):
         """Quantise k, v [(S,) n, Hkv, d] into cache tokens start .. start+n-1
         (start: a number, or int32 [S] on the device for a start per stream,
         where tokens outside the cache are dropped)."""
+        host, dev = self._at(start, "start")
         dt = k.dtype
         code = _dtype_code(dt)
         n = self._need(k, self.Hkv, "k", dt)
         self._need(v, self.Hkv, "v", dt, n)
-        host, dev = self._at(start, "start")
         back = _on(self._dev)
         try:
             rc = lib.statekv_q4_append(self._ptr, self.S, self.Hkv, self.d, self.capacity, k.data_ptr(), v.data_ptr(),
@@ -471,7 +480,7 @@ class Q4Cache:
         dt = _torch_dtype(code)
         shape = (self.S, n, self.Hkv, self.d)
         host, dev = self._at(start, "start")
-        if n < 0:
+        if _int32(n, "n") < 0:
             raise ValueError(f"negative token count {n}")
         if k is None:
             k = _empty(self._proto[dt], shape, stream)
@@ -496,6 +505,8 @@ class Q4Cache:
         q [(S,) n, Hq, d], k/v [(S,) n, Hkv, d]; with window > 0 a token at
         position p sees positions above p - window and those below n_sink.
         Returns (out, lse [(S,) Hq, n] or None)."""
+        host, dev = self._at(length, "length")
+        _int32(window, "window"), _int32(n_sink, "n_sink")
         dt = q.dtype
         code = _dtype_code(dt)
         shape = q.shape
@@ -503,7 +514,6 @@ class Q4Cache:
         n = self._need(q, Hq, "q", dt)
         self._need(k, self.Hkv, "k", dt, n)
         self._need(v, self.Hkv, "v", dt, n)
-        host, dev = self._at(length, "length")
         if out is None:
             out = torch.empty_like(q) if stream is None else _empty(q, shape, stream)
         else:
@@ -556,6 +566,7 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
     """Causal attention with a sliding window and n_sink first tokens that stay
     visible, over q [(S,) N, Hq, d], k/v [(S,) N, Hkv, d]: token i sees j <= i
     with j > i - window or j < n_sink.  Returns (out, lse [(S,) Hq, N] or None)."""
+    _int32(window, "window"), _int32(n_sink, "n_sink")
     shape, kshape, dt = q.shape, k.shape, q.dtype
     lead = (shape[0],) if len(shape) == 4 else ()
     S = shape[0] if lead else 1
