@@ -568,6 +568,8 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
     with j > i - window or j < n_sink.  Returns (out, lse [(S,) Hq, N] or None)."""
     _int32(window, "window"), _int32(n_sink, "n_sink")
     shape, kshape, dt = q.shape, k.shape, q.dtype
+    if len(shape) != 3 and len(shape) != 4:
+        raise ValueError(f"q must be [(S,) N, Hq, d], not {tuple(shape)}")
     lead = (shape[0],) if len(shape) == 4 else ()
     S = shape[0] if lead else 1
     N, Hq, d = shape[-3:]

@@ -1,5 +1,6 @@
 """Refusals of the 4-bit cache's and the windowed attention's binding that need no
-GPU: numbers that the library's 32-bit arguments do not hold."""
+GPU: numbers that the library's 32-bit arguments do not hold, tensors of too many
+or too few dimensions."""
 
 import pytest
 import torch
@@ -31,3 +32,12 @@ def test_numbers_beyond_32_bits_are_refused(x):
         for f in fs:
             with pytest.raises(ValueError, match=f"{name}=.*32 bits"):
                 f()
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 5, 4, 64), (4, 64), (64,)])
+def test_sink_window_prefill_refuses_other_dimensions(shape):
+    """Of a q with two leading dimensions only the first sequence was computed."""
+    S = _lib()
+    q, k = torch.zeros(shape), torch.zeros(5, 2, 64)
+    with pytest.raises(ValueError, match="q must be"):
+        S.sink_window_prefill(q, k, k, 4)
