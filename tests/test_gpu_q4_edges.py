@@ -342,6 +342,39 @@ def test_sink_window_prefill_of_large_values(size, d, dtype):
     check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, window, 2), dtype, P_PREFILL[dtype])
 
 
+# ---------------------------------------------------------------- many streams
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (9500, 40)])
+def test_decode_of_many_long_streams_is_shared_out(window, n_sink, dtype):
+    """70 streams of up to 12000 tokens, most of them short or empty, in a cache so
+    long that their blocks are dealt to the workers (which write partials into the
+    workspace): more streams than a warp has lanes."""
+    S, Hq, Hkv, d, cap, n = 70, 4, 2, 64, 12000, 1
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(0, 400, (S,), generator=g, dtype=torch.int32)
+    lens[::3] = 0
+    lens[[5, 31, 32, 40, 64]] = torch.tensor([12000, 7777, 8191, 11500, 9601], dtype=torch.int32)
+    lens[-2:] = 0
+    pk, pv = tokens(1, 1, cap, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    of = [(torch.roll(pk, 37 * s, 1), torch.roll(pv, 37 * s, 1)) for s in range(S)]  # every stream holds other tokens
+    c = _skv().Q4Cache(Hkv, d, cap, n_streams=S)
+    c.append(torch.cat([x[0] for x in of]).cuda(), torch.cat([x[1] for x in of]).cuda(), 0)
+    ins = [t.cuda() for t in (q, k, v, lens)]
+    out, lse = c.decode(*ins, window=window, n_sink=n_sink)
+    for _, _, ws in c._ws.values():
+        ws.view(torch.uint8).fill_(255)
+    again, _ = c.decode(*ins, window=window, n_sink=n_sink)
+    assert same(out, again) and _skv().q4_status() == 0
+    assert any((ws.view(torch.uint8) != 255).any().item() for _, _, ws in c._ws.values())
+    for s in range(S):
+        L = int(lens[s])
+        want = decode_reference(q[s], k[s], v[s], of[s][0][0, :L], of[s][1][0, :L], window, n_sink)
+        check_attention(out[s], lse[s], want, dtype, P_DECODE[dtype])
+
+
 # ------------------------------------------------------------ streams, arguments
 @cuda
 def test_a_new_cache_is_ready_for_any_stream():
