@@ -342,6 +342,38 @@ def test_sink_window_prefill_of_large_values(size, d, dtype):
     check_attention(out[0], lse[0], reference(q[0], k[0], v[0], None, None, window, 2), dtype, P_PREFILL[dtype])
 
 
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 2, 40])
+def test_decode_of_values_with_very_wide_ranges(n, dtype):
+    """Values whose scale differs by up to 2^48 between tokens, against the bounds that
+    statekv.h states: what fp16 cannot hold of a weight times a scale is off by 2^-29
+    of the largest (2^-33 in float32) times 8, a token; beyond 32 rows 2^-30 of the
+    largest weight, a token, and 2^-36 of the largest value."""
+    S, Hq, Hkv, d, L = 1, 7, 1, 128, 300
+    g = torch.Generator().manual_seed(8)
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    pv = pv * torch.exp2(torch.randint(-24, 25, (1, L, 1, 1), generator=g).float()).to(DT[dtype])
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
+    want = decode_reference(q[0], k[0], v[0], pk[0], pv[0], 0, 0)
+    logits = np.einsum("nhd,jd->nhj", O.to_f64(q[0]), O.q4_held(pk[0])[:, 0]) / np.sqrt(d)
+    weight = np.exp(logits.max(-1) - want[1].T)[..., None]          # the largest cached one, normalised
+    scale, top = O.q4_codes(pv[0])[1].max(), np.abs(O.q4_held(pv[0])).max()
+    floor = L * 8 * (2.0 ** -33 if dtype == "f32" else 2.0 ** -29) * weight * scale
+    if dtype == "bf16" and Hq * n > 32:
+        floor = L * 2.0 ** -30 * weight * top + 2.0 ** -36 * top
+    # check_attention's limits, and the floor
+    step, e = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype], 2.0 ** -19 * want[3].T[..., None]
+    lim = step * np.abs(want[0]) + want[2] * (P_DECODE[dtype] + 2 * e + (64 + want.keys / 16) * 2.0 ** -23) + floor
+    err = np.abs(O.to_f64(out[0].cpu()) - want[0])
+    fine = bool((err <= lim).all())
+    assert fine, f"out: worst {np.max(err / lim):.3g} of its limit"
+
+
 # ---------------------------------------------------------------- many streams
 @cuda
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
