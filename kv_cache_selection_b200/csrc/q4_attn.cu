@@ -288,32 +288,61 @@ __device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int 
   run(from + first, i + 1, text);
 }
 
-// One row again by a warp, token by token, where its result is not finite in the
-// groups of channels `groups`: slow, and only where sums overflow or inputs hold a
-// NaN or an infinity.  A visible NaN scale explains its group's result, which stands then.
-template <typename T, int D>
-__device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h, int g, int i, uint32_t groups) {
+// One row again by kWarps warps (all of a block's, or one), token by token, where its
+// result is not finite in the groups of channels `groups`: slow, and only where sums
+// overflow or inputs hold a NaN or an infinity.  A visible NaN scale explains its
+// group's result, which stands then.  acc, ml: shared memory for the warps' sums.
+template <typename T, int D, int kWarps>
+__device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h, int g, int i, uint32_t groups,
+                                       float (*acc)[D], float (*ml)[2]) {
   using B = Q4Block<D>;
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int E = D / 32, kScan = 8;
+  const int lane = threadIdx.x & 31, warp = kWarps == 1 ? 0 : threadIdx.x >> 5;
   const uint8_t* cache = static_cast<const uint8_t*>(a.cache) + ((long long)s * a.Hkv + g) * a.cap_blk * B::kBytes;
-  const int from = row_from(a, L, i);
+  const int from = row_from(a, L, i), sinks = min(a.n_sink, from), count = sinks + L - from;
   uint32_t nan = 0;
-  for (int j = lane; j < L; j += 32) {
-    if (j < from && j >= a.n_sink) continue;
-    const uint8_t* scales = cache + (long long)(j / kQ4Tokens) * B::kBytes + B::kVs + j % kQ4Tokens * (B::kGroups * 4);
+  for (int x0 = warp * 32 + lane; x0 < count; x0 += kWarps * 32 * kScan) {
+    uint32_t sm[kScan][B::kGroups];
 #pragma unroll
-    for (int gg = 0; gg < B::kGroups; ++gg) {
-      const float sc = q4_scale(__ldg(reinterpret_cast<const uint32_t*>(scales) + gg));
-      if (sc != sc) nan |= 1u << gg;
+    for (int b = 0; b < kScan; ++b) {
+      const int x = min(x0 + b * kWarps * 32, count - 1), j = x < sinks ? x : x - sinks + from;
+      const uint8_t* at = cache + (long long)(j / kQ4Tokens) * B::kBytes + B::kVs + j % kQ4Tokens * (B::kGroups * 4);
+#pragma unroll
+      for (int gg = 0; gg < B::kGroups; ++gg) sm[b][gg] = __ldg(reinterpret_cast<const uint32_t*>(at) + gg);
     }
-  }
-  if ((groups & ~__reduce_or_sync(0xffffffffu, nan)) == 0) return;
-  RowSum<E> sum;
-  join_own<T, D, true>(a, L, s, h, g, i, i, 0, 1, sum);
-  T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f<T>(sum.acc[e] / sum.l * (1.f / kLess));
+    for (int b = 0; b < kScan; ++b)
+#pragma unroll
+      for (int gg = 0; gg < B::kGroups; ++gg)
+        if (q4_scale(sm[b][gg]) != q4_scale(sm[b][gg])) nan |= 1u << gg;
+  }
+  if (kWarps == 1) {
+    nan = __reduce_or_sync(0xffffffffu, nan);
+  } else {
+    const int first = __syncthreads_or(nan & 1u), second = __syncthreads_or(nan & 2u);
+    nan = (first ? 1u : 0u) | (second ? 2u : 0u);
+  }
+  if ((groups & ~nan) == 0) return;
+  RowSum<E> sum;
+  join_own<T, D, true>(a, L, s, h, g, i, i, warp, kWarps, sum);
+  T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D;
+  if (kWarps == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[lane * E + e] = from_f<T>(sum.acc[e] / sum.l * (1.f / kLess));
+    return;
+  }
+  ml[warp][0] = sum.m;
+  ml[warp][1] = sum.l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = sum.acc[e];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  RowSum<1> all;
+  for (int w = 0; w < kWarps; ++w) {
+    const float v[1] = {acc[w][threadIdx.x]};
+    all.join(ml[w][0], ml[w][1], v);
+  }
+  out[threadIdx.x] = from_f<T>(all.acc[0] / all.l * (1.f / kLess));
 }
 
 // How a call is shared out: over the workers (one length, or lengths on the device),
@@ -806,7 +835,8 @@ __global__ void __launch_bounds__(warps_of<NT, NS>() * 32, 1) q4_attn_kernel(con
           out[e] = from_f<T>(sum.acc[e] / sum.l);
         }
         const unsigned again = __ballot_sync(0xffffffffu, large && sum.l == sum.l);
-        if (again) row_again<T, D>(a, vis.L, s, h, g, i, NG == 1 ? 1u : (again & 0xffffu ? 1u : 0u) | (again >> 16 ? 2u : 0u));
+        if (again)
+          row_again<T, D, 1>(a, vis.L, s, h, g, i, NG == 1 ? 1u : (again & 0xffffu ? 1u : 0u) | (again >> 16 ? 2u : 0u), nullptr, nullptr);
         if (lane == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (sum.m + log2f(sum.l)) * kLn2;
       }
       return;
@@ -901,7 +931,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const __grid
   }
   if (__syncthreads_or(large)) {
     const uint32_t first = __syncthreads_or(large && warp < 2), second = __syncthreads_or(large && warp >= 2);
-    if (warp == 0) row_again<T, D>(a, vis.L, s, h, g, i, (first ? 1u : 0u) | (second ? 2u : 0u));
+    row_again<T, D, kMergeWarps>(a, vis.L, s, h, g, i, (first ? 1u : 0u) | (second ? 2u : 0u), s_acc, s_ml);
   }
 }
 

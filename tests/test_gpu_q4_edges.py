@@ -172,6 +172,42 @@ def test_sink_window_prefill_of_nan_inputs_costs_no_more_in_float32(where):
     assert odd <= 10 * clean, f"{odd:.3f} ms against {clean:.3f}"
 
 
+@cuda
+@pytest.mark.parametrize("where", ["k", "v", "one", "text"])
+@pytest.mark.parametrize("L,n", [(300, 1), (65536, 1), (65536, 16)])
+def test_decode_of_nan_inputs_costs_no_more(L, n, where):
+    """The same for a decode over a cache that holds NaNs (everywhere, or in one group of
+    64 channels of one token), or whose text keys are NaN."""
+    S, Hq, Hkv, d = 1, 7, 1, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda m, H: torch.randn((S, m, H, d), generator=g, device="cuda").bfloat16()
+    pk, pv, k, v, q = r(L, Hkv), r(L, Hkv), r(n, Hkv), r(n, Hkv), r(n, Hq)
+
+    def ms():
+        c = _skv().Q4Cache(Hkv, d, L)
+        c.append(pk, pv, 0)
+        call = lambda: c.decode(q, k, v, L)
+        out, _ = call()
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record(), call(), b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best, out
+
+    clean, want = ms()
+    if where == "one":
+        pv[0, 5, 0, 70] = float("nan")
+    else:
+        {"k": pk, "v": pv, "text": k}[where][:] = float("nan")
+    odd, out = ms()
+    assert torch.isnan(out[..., 64:] if where == "one" else out).all()
+    if where == "one":
+        assert same(out[..., :64], want[..., :64])
+    assert odd <= 10 * clean, f"{odd:.3f} ms against {clean:.3f}"
+
+
 # -------------------------------------------- tokens that only some rows see
 @cuda
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
