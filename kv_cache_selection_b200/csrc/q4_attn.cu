@@ -87,11 +87,6 @@ constexpr int kOwnText = 32;  // most text tokens of a call whose thread blocks 
 
 __device__ int g_err;  // first error of the ring's waits of all calls on a device
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -439,7 +434,7 @@ __global__ void __launch_bounds__(most_threads<D, NT, NS>(), 1) q4_attn_kernel(c
     auto issue = [&](int v, int n) {
       const uint32_t bar = bars + 8u * (n % kStages);
       tc::mbar_arrive_expect_tx(bar, B::kBytes);
-      bulk_load(ring_u32 + (n % kStages) * B::kBytes, base + (long long)vis.block(v) * B::kBytes, B::kBytes, bar);
+      tc::bulk_load(ring_u32 + (n % kStages) * B::kBytes, base + (long long)vis.block(v) * B::kBytes, B::kBytes, bar);
     };
     int issued = done;
     if (lane == 0)

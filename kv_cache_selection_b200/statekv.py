@@ -453,7 +453,8 @@ class Q4Cache:
         if isinstance(at, torch.Tensor):
             self._need_like(at, (self.S,), torch.int32, name)
             return 0, at.data_ptr()
-        return _int32(int(at), name), None
+        at = int(at)
+        return (_int32(at, name) if at >> 31 else at), None
 
     def append(self, k, v, start, stream=None):
         """Quantise k, v [(S,) n, Hkv, d] into cache tokens start .. start+n-1
@@ -506,7 +507,8 @@ class Q4Cache:
         position p sees positions above p - window and those below n_sink.
         Returns (out, lse [(S,) Hq, n] or None)."""
         host, dev = self._at(length, "length")
-        _int32(window, "window"), _int32(n_sink, "n_sink")
+        if (window | n_sink) >> 31:  # (negative ones are the library's to refuse)
+            _int32(window, "window"), _int32(n_sink, "n_sink")
         dt = q.dtype
         code = _dtype_code(dt)
         shape = q.shape
@@ -566,7 +568,8 @@ def sink_window_prefill(q, k, v, window, n_sink=0, out=None, lse=None, with_lse=
     """Causal attention with a sliding window and n_sink first tokens that stay
     visible, over q [(S,) N, Hq, d], k/v [(S,) N, Hkv, d]: token i sees j <= i
     with j > i - window or j < n_sink.  Returns (out, lse [(S,) Hq, N] or None)."""
-    _int32(window, "window"), _int32(n_sink, "n_sink")
+    if (window | n_sink) >> 31:  # (negative ones are the library's to refuse)
+        _int32(window, "window"), _int32(n_sink, "n_sink")
     shape, kshape, dt = q.shape, k.shape, q.dtype
     if len(shape) != 3 and len(shape) != 4:
         raise ValueError(f"q must be [(S,) N, Hq, d], not {tuple(shape)}")
