@@ -17,7 +17,8 @@
 // head times the text tokens, eight to a tile.
 //   Q: scaled by a power of two per row (largest element in [2^10, 2^11)); bf16
 //     values are then exact in fp16, float32 ones are split into two fp16 parts
-//     (NS = 2), 22 bits.
+//     (NS = 2), 22 bits.  S is summed in units of 2^18, which keep it in range
+//     whatever the keys.
 //   P s: in fp16 relative to the largest V scale met so far (a power of two
 //     R_g per group, lazily raised as the row maximum is): 2^-11 off at most,
 //     an eighth of what the bf16 result rounds by; float32 again takes two parts.
@@ -43,12 +44,12 @@
 // thread block of its own, which writes the results itself.
 //
 // Measured (B200, graph replays, bf16, d = 128, G = 7, one text token, caches beyond
-// L2): 4 ragged streams of up to 131072 tokens, 4 KV heads, 55.5 us (4.4 TB/s of
+// L2): 4 ragged streams of up to 131072 tokens, 4 KV heads, 53.7 us (4.6 TB/s of
 // the cache; 245 MB would take 37.4 at the copy rate), 131072 tokens of one stream
-// 26.7 us (75 MB: 11.5).  About 8 us of each are the first copies' latency and the
+// 24.6 us (75 MB: 11.5).  About 8 us of each are the first copies' latency and the
 // merge; the loop streams at some 5 TB/s, the tensor-core and integer pipes each
-// half busy and 12 warps an SM too few to hide the latencies between them; with 8
-// warps 61.5, with 16 (three stages each) 57.5 us.
+// half busy and 12 warps an SM too few to hide the latencies between them (measured
+// apart, at 56.5 us: with 8 warps 61.5, with 16, three stages each, 57.5).
 #include <algorithm>
 #include <type_traits>
 

@@ -28,10 +28,10 @@
 // moves between threads.
 //
 // Measured (B200, graph replays, bf16, d = 128, 4 KV heads, 16 text tokens of G = 7
-// over 131072 tokens): 61.5 us (30.1 GFLOP: 18.2 us of the tensor cores).  A quarter
-// is the exponents' pass over the scales and the first copies; then a key tile
-// takes 2800 cycles, of which the softmax 2500 (its halves are in step, so that
-// its exponentials, 1024 cycles, meet nobody else's).
+// over 131072 tokens): 60.0 us (30.1 GFLOP: 18.2 us of the tensor cores).  15 % is the
+// exponents' pass over the scales and the first copies (17000 of 115000 cycles); then
+// a key tile takes 2800 cycles, of which the softmax 2500 (its halves are in step, so
+// that its exponentials, 1024 cycles, meet nobody else's).
 #include <type_traits>
 
 #include "common.cuh"

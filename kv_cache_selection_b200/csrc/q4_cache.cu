@@ -5,11 +5,13 @@
 // covered by an append is read, merged and written by the one thread block that
 // owns it; no two thread blocks of a call share a word.
 //
-// Measured (B200, graph replays, 131072 tokens of 4 heads, d = 128, bf16, inputs
-// beyond L2): append 99 us (268 MB in, 75 MB out: 3.5 TB/s), bound by instructions
-// (82 % of the issue slots; the group ranges, exact ties and the packing), read 58
-// us (5.9 TB/s), bound by memory writes.  Sizes that no longer fill the SMs are bound by
-// latency: a 256-token frame appends in 8.3 us, a launch and four dependent passes.
+// Measured (B200, graph replays, 131072 tokens of 4 heads, d = 128, inputs beyond
+// L2): append in bf16 94 us (268 MB in, 75 MB out: 3.7 TB/s), bound by instructions
+// (82 % of the issue slots; the group ranges, exact ties and the packing), in float32
+// 110 us (537 MB in: 5.6 TB/s); read in bf16 58 us (5.9 TB/s), in float32 139 us (4.4
+// TB/s), bound by memory writes.  Sizes that no longer fill the SMs are bound by
+// latency: a 256-token frame is appended and read back in 6.5 us, two launches of four
+// dependent passes and one.
 #include "common.cuh"
 #include "kernels.h"
 #include "q4_cache.cuh"

@@ -26,7 +26,7 @@
 // where the inputs hold a NaN, an infinity or values that large).
 //
 // Measured (B200): 65536 tokens, 28 heads, d = 128, window 4096: 3365 us, 1112
-// TFLOP/s; 4 x 4001 tokens, 14 heads, d = 64, window 1024: 130 us, 396 TFLOP/s.  At
+// TFLOP/s; 4 x 4001 tokens, 14 heads, d = 64, window 1024: 125 us, 413 TFLOP/s.  At
 // d = 128 a pair of key tiles takes 3650 cycles for 2048 of products and 2048 of
 // exponentials: the bound is the chain S -> softmax (2180 cycles, half of them
 // exponentials) -> P V -> next S of each query tile, with two in flight.  At d = 64
