@@ -291,10 +291,15 @@ __device__ __forceinline__ void join_own(const WindowArgs& a, int L, int s, int 
   run(from + first, i + 1, text);
 }
 
+// Row maxima (log2) from which on the weights may be too small to hold (reference_of).
+constexpr float kHuge = 0x1p22f;
+constexpr uint32_t kAllGroups = 7u;  // whatever their values
+
 // One row again by kWarps warps (all of a block's, or one), token by token, where its
-// result is not finite in the groups of channels `groups`: slow, and only where sums
-// overflow or inputs hold a NaN or an infinity.  A visible NaN scale explains its
-// group's result, which stands then.  acc, ml: shared memory for the warps' sums.
+// result is not finite in the groups of channels `groups`, or its logits are huge:
+// slow, and only where sums overflow or inputs hold a NaN, an infinity or keys and
+// queries far beyond the usual.  A visible NaN scale explains its group's result,
+// which stands then.  acc, ml: shared memory for the warps' sums.
 template <typename T, int D, int kWarps>
 __device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h, int g, int i, uint32_t groups,
                                        float (*acc)[D], float (*ml)[2]) {
@@ -329,7 +334,9 @@ __device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h,
   RowSum<E> sum;
   join_own<T, D, true>(a, L, s, h, g, i, i, warp, kWarps, sum);
   T* out = static_cast<T*>(a.out) + (((long long)s * a.n + i) * a.Hq + h) * D;
+  float* lse = a.lse ? a.lse + ((long long)s * a.Hq + h) * a.n + i : nullptr;
   if (kWarps == 1) {
+    if (lane == 0 && lse) *lse = (sum.m + log2f(sum.l)) * kLn2;
 #pragma unroll
     for (int e = 0; e < E; ++e) out[lane * E + e] = from_f<T>(sum.acc[e] / sum.l * (1.f / kLess));
     return;
@@ -346,6 +353,7 @@ __device__ __noinline__ void row_again(const WindowArgs& a, int L, int s, int h,
     all.join(ml[w][0], ml[w][1], v);
   }
   out[threadIdx.x] = from_f<T>(all.acc[0] / all.l * (1.f / kLess));
+  if (threadIdx.x == 0 && lse) *lse = (all.m + log2f(all.l)) * kLn2;
 }
 
 // How a call is shared out: over the workers (one length, or lengths on the device),
@@ -656,11 +664,11 @@ __global__ void __launch_bounds__(most_threads<D, NT, NS>(), 1) q4_attn_kernel(c
             float top = fmaxf(fmaxf(t[nt][0][e], t[nt][0][2 + e]), fmaxf(t[nt][1][e], t[nt][1][2 + e]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float nm = fmaxf(m[nt][e], top * rs[nt][e]);
+            const float nm = fmaxf(m[nt][e], tc::reference_of(top * rs[nt][e]));
             fo[nt][e] = nm == m[nt][e] ? 1.f : tc::ex2_approx(m[nt][e] - nm);
             m[nt][e] = nm;
             mr[nt][e] = nm == -INFINITY ? 0.f : nm;
-            above[nt][e] = (nm + kRaise) / rs[nt][e];
+            above[nt][e] = (fmaf(fabsf(nm), -0x1p-21f, nm) + kRaise) / rs[nt][e];
             l[nt][e] *= fo[nt][e];
 #pragma unroll
             for (int gg = 0; gg < NG; ++gg) corr[nt][gg][e] *= fo[nt][e];
@@ -838,9 +846,10 @@ __global__ void __launch_bounds__(most_threads<D, NT, NS>(), 1) q4_attn_kernel(c
           out[e] = from_f<T>(sum.acc[e] / sum.l);
         }
         const unsigned again = __ballot_sync(0xffffffffu, large && sum.l == sum.l);
-        if (again)
-          row_again<T, D, 1>(a, vis.L, s, h, g, i, NG == 1 ? 1u : (again & 0xffffu ? 1u : 0u) | (again >> 16 ? 2u : 0u), nullptr, nullptr);
         if (lane == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (sum.m + log2f(sum.l)) * kLn2;
+        uint32_t groups = NG == 1 ? (again ? 1u : 0u) : (again & 0xffffu ? 1u : 0u) | (again >> 16 ? 2u : 0u);
+        if (fabsf(sum.m) >= kHuge) groups = kAllGroups;
+        if (groups) row_again<T, D, 1>(a, vis.L, s, h, g, i, groups, nullptr, nullptr);
       }
       return;
     }
@@ -932,9 +941,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const __grid
     if (d == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (mx + log2f(ls)) * kLn2;
     large = !(fabsf(o) < INFINITY) && ls == ls;
   }
-  if (__syncthreads_or(large)) {
-    const uint32_t first = __syncthreads_or(large && warp < 2), second = __syncthreads_or(large && warp >= 2);
-    row_again<T, D, kMergeWarps>(a, vis.L, s, h, g, i, (first ? 1u : 0u) | (second ? 2u : 0u), s_acc, s_ml);
+  if (__syncthreads_or(large || fabsf(mx) >= kHuge)) {
+    const int first = __syncthreads_or(large && warp < 2), second = __syncthreads_or(large && warp >= 2);
+    row_again<T, D, kMergeWarps>(a, vis.L, s, h, g, i, fabsf(mx) >= kHuge ? kAllGroups : (first ? 1u : 0u) | (second ? 2u : 0u),
+                                 s_acc, s_ml);
   }
 }
 

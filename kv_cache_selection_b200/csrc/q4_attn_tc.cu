@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
           for (int jj = 0; jj < 8; jj += 2)
             m4[q4] = max3f(m4[q4], __uint_as_float(sv[8 * q4 + jj]), __uint_as_float(sv[8 * q4 + jj + 1]));
       }
-      const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]) * c;
+      const float mx = reference_of(fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]) * c);
       // both halves learn whether one of them asks for a raise, or gave up
       if (named_bar_red_or(3, 256, !ok || mx > m_used + kRaise)) {
         half_max[half * 128 + r] = mx;

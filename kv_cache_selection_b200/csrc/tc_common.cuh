@@ -275,6 +275,12 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// A row maximum x (log2) to subtract from the logits t c in one fma, whose product is
+// exact: x with 2^-21 of it on top, so that no rounding (of x, or of a bound derived
+// from it) leaves a difference above the bound's.  Whatever the logits' size, no
+// weight overflows; where they are beyond 2^22, the largest ones are small, down to 0.
+__device__ __forceinline__ float reference_of(float x) { return fmaxf(fmaf(fabsf(x), 0x1p-21f, x), x); }
+
 // Bounded wait used on teardown paths only: ignores the abort flag.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int* err) {
   const unsigned long long t0 = globaltimer_ns();

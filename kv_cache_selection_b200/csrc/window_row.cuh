@@ -11,10 +11,11 @@ namespace skv {
 // The row's result is in `out` already.  What of it is not finite may come from
 //   - a visible value that is a NaN or an infinity: it stands;
 //   - a hidden one of a shared tile, which entered a product with weight 0;
-//   - sums of large weighted values that overflowed, where their mean does not.
+//   - sums of large weighted values that overflowed, where their mean does not;
+//   - a sum of weights that is 0, of huge logits (reference_of).
 // The first is looked for beforehand, so that inputs with NaNs cost one pass over
-// the values at most; the other two are computed again, weights in units of 2^24 (as
-// many tokens as a sequence can have).  The row's lse is right as it is.
+// the values at most; the others are computed again, weights in units of 2^24 (as
+// many tokens as a sequence can have).
 template <typename T, int D>
 __device__ __noinline__ void window_row_again(const WindowArgs& a, int s, int h, int i) {
   constexpr int E = D / 32;  // channels of a lane
@@ -98,6 +99,7 @@ __device__ __noinline__ void window_row_again(const WindowArgs& a, int s, int h,
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = from_f<T>(o[e] / l * (1.f / kLess));
+  if (lane == 0 && a.lse) a.lse[((long long)s * a.Hq + h) * a.n + i] = (m + log2f(l)) * kLn2;
 }
 
 }  // namespace skv

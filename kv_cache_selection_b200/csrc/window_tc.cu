@@ -23,7 +23,8 @@
 // A hidden value enters P V with weight 0, and 0 x NaN is NaN, and sums of values next
 // to the largest float overflow: a row that ends with an output that is not finite,
 // though its sum of weights is, goes through window_row_again (slow, and only
-// where the inputs hold a NaN, an infinity or values that large).
+// where the inputs hold a NaN, an infinity or values that large, or where logits
+// beyond 2^27 leave no weight to hold).
 //
 // Measured (B200): 65536 tokens, 28 heads, d = 128, window 4096: 3365 us, 1112
 // TFLOP/s; 4 x 4001 tokens, 14 heads, d = 64, window 1024: 125 us, 413 TFLOP/s.  At
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m8[q8] = fmaxf(m8[q8], __uint_as_float(sv[16 * q8 + 15]));
       }
       const float mx = fmaxf(fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5])), fmaxf(m8[6], m8[7]));
-      const float m_new = fmaxf(m_used, mx * c);
+      const float m_new = fmaxf(m_used, reference_of(mx * c));
       const bool raise = m_new > m_used + kRaise;
       if (__any_sync(0xffffffffu, raise)) {
         const float f = raise ? ex2_approx(m_used - m_new) : 1.f;

@@ -365,6 +365,68 @@ def test_decode_of_large_and_poisoned_values_in_a_window(n, L, dtype):
     check_attention(got[0], lse[0], want, dtype, P_DECODE[dtype])
 
 
+def huge_rows(out, lse, q, k, v, keys, values, at, signs, dtype, p_step):
+    """Rows over keys that include a huge one, all channels alike, at `at`: heads of
+    sign 1 take its value, heads of sign -1 what the other tokens make (0: not
+    checked).  The value is off by its own rounding and by that of the weight times
+    its scale, 2^-11 or in float32 2^-22 of P |(c - 8) s|, at most P (|v| + |mid|) and so
+    3 max |v| with P = 1; 128-row calls round v and mid instead, the same bound."""
+    n, Hq, d = q.shape
+    step, other = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}[dtype], np.arange(len(keys)) != at
+    weight = max(p_step, 2.0 ** -22)
+    got, glse, qd = O.to_f64(out.cpu()), O.to_f64(lse.cpu()), O.to_f64(q)
+    for h, sign in enumerate(signs):
+        if sign > 0:
+            want = np.broadcast_to(values[at, 0], (n, d))
+            logit = qd[:, h] @ keys[at, 0] / np.sqrt(d)
+            assert (np.abs(got[:, h] - want) <= step * np.abs(want) + weight * 3 * np.abs(values[at, 0]).max()).all()
+            assert (np.abs(glse[h] - logit) <= 2.0 ** -19 * np.abs(logit)).all()
+        elif sign < 0:
+            w = reference(q[:, h:h + 1], k, v, keys[other], values[other], 0, 0)
+            part = Want((w[0], w[1], 2 * w[2] + np.abs(values).max(), w[3]))
+            part.keys = w.keys
+            check_attention(out[:, h:h + 1], lse[h:h + 1], part, dtype, p_step)
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,n,L", LARGE)
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e10, 1e20])
+def test_decode_of_huge_logits(size, Hq, n, L, dtype):
+    """A key so large that its logits are beyond float32's integers."""
+    S, Hkv, d, at = 1, 1, 128, 37
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    signs = [1 if h % 2 else -1 for h in range(Hq)]
+    q = torch.randn(S, n, Hq, d, generator=torch.Generator().manual_seed(3)) + 2 * torch.tensor(signs)[:, None]
+    q = q.to(DT[dtype])
+    pk[:, at] = size
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
+    if dtype == "bf16" and Hq * n > 32 and size > 1e7:   # the header: keys below 2^-26 of the largest lose bits
+        signs = [max(x, 0) for x in signs]
+    huge_rows(out[0], lse[0], q[0], k[0], v[0], O.q4_held(pk[0]), O.q4_held(pv[0]), at, signs, dtype,
+              P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e10, 1e20])
+def test_sink_window_prefill_of_huge_logits(size, d, dtype):
+    n, Hq, Hkv, at = 300, 4, 1, 1
+    k, v = tokens(1, 1, n, Hkv, d, dtype)
+    signs = [1 if h % 2 else -1 for h in range(Hq)]
+    q = torch.randn(1, n, Hq, d, generator=torch.Generator().manual_seed(3)) + 2 * torch.tensor(signs)[:, None]
+    q = q.to(DT[dtype])
+    k[:, at] = size
+    out, lse = _skv().sink_window_prefill(q.cuda(), k.cuda(), v.cuda(), n)
+    past = 2                                 # the rows from here on see it
+    huge_rows(out[0, past:], lse[0][:, past:], q[0, past:], k[0, past:], v[0, past:], O.to_f64(k[0, :past]), O.to_f64(v[0, :past]),
+              at, signs, dtype, P_PREFILL[dtype])
+
+
 @cuda
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
