@@ -354,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     float m_used = -INFINITY, l = 0.f, c = 0.f;
     bool ok = n > 0;
     if (ok) {
-      // (finite: the largest queries and keys need not meet in a channel)
-      c = fminf(reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK), 0x1.fffffep127f);
+      // (finite: the largest queries and keys need not meet in a channel; and above 0,
+      // for hidden columns of -inf: where it is raised, logits are below 2^-90)
+      c = fminf(fmaxf(reinterpret_cast<const float*>(smem + L::kRow)[r] * exp2i(eK), 0x1p-126f), 0x1.fffffep127f);
       if (half == 0) {
         // the row's sums of q for the product of depth 16: per group hi hi lo lo,
         // against m + 8 s as hi lo hi lo (a factor of 4 moved over: fp16's range)

@@ -365,6 +365,26 @@ def test_decode_of_large_and_poisoned_values_in_a_window(n, L, dtype):
     check_attention(got[0], lse[0], want, dtype, P_DECODE[dtype])
 
 
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [5, 30])
+@pytest.mark.parametrize("e", [40, 100, 118])
+def test_decode_of_tiny_queries_that_see_no_cached_token(e, window, dtype):
+    """More than 32 rows whose tile sees nothing of the cache, queries of 2^-e and text
+    keys of 2^e."""
+    S, Hq, Hkv, d, L, n = 1, 8, 1, 64, 33, 50
+    pk, pv = tokens(1, S, L, Hkv, d, dtype)
+    k, v = tokens(2, S, n, Hkv, d, dtype)
+    q, _ = tokens(3, S, n, Hq, d, dtype, loud=False)
+    pk, k, q = pk * 2.0 ** e, k * 2.0 ** e, q * 2.0 ** -e
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    for past in (L, 0):
+        out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), past, window=window)
+        check_attention(out[0], lse[0], decode_reference(q[0], k[0], v[0], pk[0, :past], pv[0, :past], window, 0), dtype,
+                        P_DECODE[dtype])
+
+
 def huge_rows(out, lse, q, k, v, keys, values, at, signs, dtype, p_step):
     """Rows over keys that include a huge one, all channels alike, at `at`: heads of
     sign 1 take its value, heads of sign -1 what the other tokens make (0: not
