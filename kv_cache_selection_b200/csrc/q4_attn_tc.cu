@@ -15,7 +15,7 @@
 // Keys and values are scaled by powers of two that bring the largest magnitude in
 // the block's range of tokens (read off the scales beforehand) into [2^12, 2^13),
 // so fp16 serves the cache's range: full precision down to 2^-26 of the largest.
-//   K: (c - 8) s has 11 bits and is exact in fp16; the groups' m + 8 s times the
+//   K: (c - 8) s has 11 bits and is exact in fp16 (down to that); the groups' m + 8 s times the
 //     sums of q enter as one more product of depth 16, both sides in two fp16
 //     parts.  So S is as exact as its float32 sums.
 //   V: (c - 8) s + (m + 8 s) in one fp16 fma, 2^-11 of a value.
@@ -490,8 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_attn_tc_kernel(Q4AttnArgs p) {
     } else if (real) {  // no tiles (or an abandoned call): nothing to add
       for (int d = 0; d < D / 2; d += 4) *reinterpret_cast<float4*>(po + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // An infinite maximum has the merge take the row again.  Beside keys of 2^12 small
+    // ones are held to 2^-22 (8 times a scale's 2^-25), which 128 channels of q below
+    // 2^11 make 2^-4 of S, so a logit is off by up to c 2^-4: 2^-11, with c below 2^-7
+    // (largest logits of some 10^5; usual ones have 2^-17).
     if (real && half == 0)
-      *reinterpret_cast<float2*>(p.part_ml + at * 2) = ok ? make_float2(m_used, l * exp2i(-kPShift)) : make_float2(-INFINITY, 0.f);
+      *reinterpret_cast<float2*>(p.part_ml + at * 2) =
+          !ok ? make_float2(-INFINITY, 0.f) : c >= 0x1p-7f ? make_float2(INFINITY, 0.f) : make_float2(m_used, l * exp2i(-kPShift));
   } else if (warp < 16) {
     // ------------------------------------------------------- dequantise K
     const int w4 = warp & 3, tid = w4 * 32 + lane;

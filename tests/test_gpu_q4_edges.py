@@ -424,10 +424,30 @@ def test_decode_of_huge_logits(size, Hq, n, L, dtype):
     c = _skv().Q4Cache(Hkv, d, L)
     c.append(pk.cuda(), pv.cuda(), 0)
     out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
-    if dtype == "bf16" and Hq * n > 32 and size > 1e7:   # the header: keys below 2^-26 of the largest lose bits
-        signs = [max(x, 0) for x in signs]
     huge_rows(out[0], lse[0], q[0], k[0], v[0], O.q4_held(pk[0]), O.q4_held(pv[0]), at, signs, dtype,
               P_DECODE[dtype])
+
+
+@cuda
+@pytest.mark.parametrize("size", [1e3, 3e4, 1e6, 1e10, 1e20])
+def test_decode_of_many_rows_beside_a_huge_key(size):
+    """Rows that a huge visible key weighs nothing for keep the logits of the others:
+    queries away from it, 280 rows."""
+    S, Hq, Hkv, d, n, L, at = 1, 7, 1, 128, 40, 900, 37
+    pk, pv = tokens(1, S, L, Hkv, d, "bf16")
+    k, v = tokens(2, S, n, Hkv, d, "bf16")
+    q = (torch.randn(S, n, Hq, d, generator=torch.Generator().manual_seed(3)) - 2).bfloat16()
+    pk[:, at] = size
+    c = _skv().Q4Cache(Hkv, d, L)
+    c.append(pk.cuda(), pv.cuda(), 0)
+    out, lse = c.decode(q.cuda(), k.cuda(), v.cuda(), L)
+    other = torch.arange(L) != at
+    want = decode_reference(q[0], k[0], v[0], pk[0, other], pv[0, other], 0, 0)
+    e = 2.0 ** -11                           # what statekv.h allows a logit
+    wide = Want((want[0], want[1], want[2] * (1 + 2 * e / P_DECODE["bf16"]), want[3]))
+    wide.keys = want.keys
+    check_attention(out[0], None, wide, "bf16", P_DECODE["bf16"])
+    assert (np.abs(O.to_f64(lse[0].cpu()) - want[1]) <= e + 2.0 ** -19 * want[3] + 2.0 ** -20 + 2.0 ** -23 * np.abs(want[1])).all()
 
 
 @cuda
