@@ -340,8 +340,8 @@ int statekv_step_noalloc(int Hq, int Hkv, int d, int T, int B, int dtype, int ma
  *   s = (largest - m) / 15 rounded up to bfloat16,
  *   c = the integer nearest to (x - m) / s, ties to even (0 where s = 0),
  * so the error is at most s / 2 and a group of equal bfloat16 values is exact.
- * With s and m that is 4.5 bits a value.  A group that holds a NaN or an
- * infinity reads back as NaN.
+ * With s and m that is 4.5 bits a value.  A group that holds a NaN, an infinity or
+ * a float32 value below the least bfloat16 (-3.39e38) reads back as NaN.
  *
  * The cache is one buffer of statekv_q4_bytes bytes (16-byte aligned) for
  * n_streams sequences of up to `capacity` tokens each; its inner layout is the

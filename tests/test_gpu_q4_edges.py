@@ -589,3 +589,31 @@ def test_a_new_handle_is_ready_for_any_stream(detailed):
         if detailed == "native":
             assert same(D["k"][0, :, :T].cpu(), k[0].transpose(0, 1).contiguous())
         h.close()
+
+
+# ------------------------------------------------------------ writing and reading
+@cuda
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["bits", "powers", "mixed", "subnormal", "offset", "two"])
+def test_append_of_any_numbers(kind, dtype):
+    """Random bit patterns, magnitudes from the least subnormal number up, groups of one
+    small range far from 0, groups of two values: the held values are the oracle's."""
+    g = np.random.default_rng(7)
+    n, H, d = 300, 2, 128
+    shape = (1, n, H, d)
+    x = {"bits": lambda: g.integers(0, 2 ** 32, shape, dtype=np.uint64).astype(np.uint32).view(np.float32).copy(),
+         "powers": lambda: g.standard_normal(shape) * np.exp2(g.integers(-149, 120, (1, n, H, 1))),
+         "mixed": lambda: g.standard_normal(shape) * np.exp2(g.integers(-20, 20, shape)),
+         "subnormal": lambda: g.standard_normal(shape) * 2.0 ** -140,
+         "offset": lambda: 1e30 + 1e24 * g.standard_normal(shape),
+         "two": lambda: np.where(g.random(shape) < 0.5, 1, -1) * np.exp2(g.integers(-140, 127, (1, n, H, 1)))}[kind]()
+    with np.errstate(over="ignore"):
+        t = torch.from_numpy(np.asarray(x, dtype=np.float32)).to(DT[dtype])
+    t = torch.where(t.float() < -3.38e38, torch.zeros_like(t), t)    # (below the least bfloat16: NaN)
+    c = _skv().Q4Cache(H, d, n)
+    c.append(t.cuda(), (-t).clamp(min=-3.38e38).cuda(), 0)
+    for got, src in zip(c.read(0, n, dtype="f32"), (t, (-t).clamp(min=-3.38e38))):
+        want = exact_tensor(O.q4_held(src.float()), "f32")
+        got = got.cpu()
+        fine = bool(((got == want) | (torch.isnan(got) & torch.isnan(want))).all())
+        assert fine, kind
